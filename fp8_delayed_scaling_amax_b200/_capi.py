@@ -36,6 +36,11 @@ class fp8_ring_t(Structure):
                 ("fp8_max", c_float), ("pow2_margin", c_float)]
 
 
+class fp8_block_scale_t(Structure):
+    _fields_ = [("scale", c_void_p), ("block_mn", c_int), ("stride_mn", c_int64), ("stride_kb", c_int64),
+                ("stride_batch", c_int64)]
+
+
 _P = c_void_p
 _SIGNATURES = {
     "fp8_scale_ring_init": (c_int, [_P, c_int, _P]),
@@ -75,6 +80,11 @@ _SIGNATURES = {
     "linear_backward_fp8_saved_t": (c_int, [_P, _P, _P, c_int64, c_int64, c_int64, c_int, c_int, c_int, c_int, c_int,
                                             _P, _P, POINTER(fp8_ring_t), c_float, _P, _P, c_size_t, _P, _P, _P,
                                             _P]),
+    "fp8_quantize_block": (c_int, [_P, c_int, c_int64, c_int64, c_int, _P, _P, _P, _P, _P]),
+    "fp8_quantize_block128": (c_int, [_P, c_int, c_int64, c_int64, c_int, _P, _P, _P]),
+    "fp8_gemm_block": (c_int, [_P, _P, c_int, c_int, c_int, c_int64, c_int64, c_int64, c_int64, c_int64, c_int64,
+                               c_int64, c_int64, c_int64, c_int64, POINTER(fp8_block_scale_t),
+                               POINTER(fp8_block_scale_t), _P, _P, _P]),
     "fp8_get_device_status": (c_int, [_P, POINTER(c_int)]),
     "fp8_set_wait_timeout_ns": (c_int, [c_uint64]),
     "fp8_debug_stalled_wait": (c_int, [_P]),
@@ -327,6 +337,49 @@ def linear_backward_fp8_saved_t(g, x8t, w8t, m, k, n, fmt, fmt_t, need_grad_x, n
         int(bool(need_grad_w)), int(bool(need_grad_b)), _ptr(sx), _ptr(sw), _ring(g_ring), float(pow2_margin),
         _ptr(sg_used), _ptr(workspace), int(workspace_bytes), _ptr(grad_x), _ptr(grad_w), _ptr(grad_b),
         _stream(stream)))
+
+
+class BlockScale:
+    """Host description of a block-scaled operand's scales (``fp8_block_scale_t``): the fp32 tensor
+    and its strides in elements; ``block_mn`` is 1 (a scale per row) or 128."""
+
+    def __init__(self, scale, block_mn: int, stride_mn: int, stride_kb: int, stride_batch: int = 0):
+        self.scale = scale
+        self.block_mn = int(block_mn)
+        self.stride_mn = int(stride_mn)
+        self.stride_kb = int(stride_kb)
+        self.stride_batch = int(stride_batch)
+
+    def as_c(self) -> fp8_block_scale_t:
+        return fp8_block_scale_t(_ptr(self.scale), self.block_mn, self.stride_mn, self.stride_kb, self.stride_batch)
+
+
+def _block_scale(s):
+    if s is None:
+        return None
+    return ctypes.byref(s if isinstance(s, fp8_block_scale_t) else s.as_c())
+
+
+def fp8_quantize_block(x, in_type, rows, cols, fmt, out_row, scale_row, out_col=None, scale_col=None, stream=None):
+    """Block quantize with 1 x 128 blocks (out_row, scale_row) and / or 128 x 1 blocks (out_col, scale_col)."""
+    return _check("fp8_quantize_block", lib().fp8_quantize_block(
+        _ptr(x), int(in_type), int(rows), int(cols), int(fmt), _ptr(out_row), _ptr(scale_row), _ptr(out_col),
+        _ptr(scale_col), _stream(stream)))
+
+
+def fp8_quantize_block128(x, in_type, rows, cols, fmt, out, scale, stream=None):
+    """Block quantize with 128 x 128 blocks."""
+    return _check("fp8_quantize_block128", lib().fp8_quantize_block128(
+        _ptr(x), int(in_type), int(rows), int(cols), int(fmt), _ptr(out), _ptr(scale), _stream(stream)))
+
+
+def fp8_gemm_block(a, b, fmt_a, fmt_b, layout, m, n, k, lda, ldb, ldo, batch, stride_a, stride_b, stride_o, scale_a,
+                   scale_b, bias, out, stream=None):
+    """Product of block-scaled operands; scale_a / scale_b are :class:`BlockScale`."""
+    return _check("fp8_gemm_block", lib().fp8_gemm_block(
+        _ptr(a), _ptr(b), int(fmt_a), int(fmt_b), int(layout), int(m), int(n), int(k), int(lda), int(ldb), int(ldo),
+        int(batch), int(stride_a), int(stride_b), int(stride_o), _block_scale(scale_a), _block_scale(scale_b),
+        _ptr(bias), _ptr(out), _stream(stream)))
 
 
 def fp8_get_device_status(stream=None) -> int:

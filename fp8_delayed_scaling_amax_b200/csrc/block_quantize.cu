@@ -1,0 +1,354 @@
+// FP8 quantize with one scale per block of 128: rows of 1 x 128, columns of 128 x 1, both from one
+// read, or 128 x 128 blocks.
+//
+// For a block S of x (any subset of the elements of one 128 x 128 tile):
+//     s = max(RN32(max_S |x| / FP8_MAX), 1e-12),   q = RN_fp8(RN32(x * RN32(1/s))), saturating,
+// the formula of the dynamic step (fp8_amax_scale with margin 0) and of fp8_quantize, per block.
+//
+// Every mode walks 128 x 128 tiles, one per 256-thread CTA: a tile holds whole blocks of either
+// orientation, so no reduction ever leaves the CTA and no scratch or atomic is needed.  Thread
+// (tx, ty) holds columns 8 tx .. 8 tx + 7 of rows ty + 16 r, r = 0 .. 7, in registers (a warp reads
+// two 256-byte row pieces of bf16 per load, all eight loads in flight): a row's maximum is a
+// 16-lane shuffle, a column's one shuffle and an 8-warp shared-memory maximum.  x is read once for
+// both orientations, and the column sums of the tile (the bias gradient's partial sums) come
+// from the same registers.  Bound by HBM: 2 bytes in and 1 out per bf16 element and orientation.
+#include <cuda_runtime.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include <string>
+
+#include "internal.h"
+
+namespace fp8dsa {
+namespace {
+
+constexpr int kB = 128;         // block and tile edge
+constexpr int kThreads = 256;
+constexpr int kRowsPer = 8;     // rows per thread
+constexpr int kColsPer = 8;     // columns per thread
+
+struct BlockQuantArgs {
+    const void* x;
+    int64_t rows, cols;
+    int64_t tiles_c;
+    uint8_t* out_row;   // 1 x 128 blocks (or 128 x 128 blocks in kSquare)
+    float* scale_row;   // [tiles_c][rows] (kSquare: [tiles_r][tiles_c])
+    uint8_t* out_col;   // 128 x 1 blocks
+    float* scale_col;   // [tiles_r][cols]
+    float* colsum;      // [tiles_r][cols] column sums of each tile, or null
+    int vec_in;         // 16-byte loads
+    int vec_row, vec_col;  // 8-byte stores
+};
+
+__device__ __forceinline__ void block_step(float amax, float fp8_max, float& s, float& inv) {
+    s = fmaxf(__fdiv_rn(amax, fp8_max), 1e-12f);
+    inv = __frcp_rn(s);
+}
+
+// 8 elements of row `row` from column `col` on (zeros outside the tensor) as fp32.
+template <int kIn>
+__device__ __forceinline__ void load8(const BlockQuantArgs& g, int64_t row, int64_t col, float (&v)[8]) {
+    if (row >= g.rows || col >= g.cols) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = 0.0f;
+        return;
+    }
+    const int64_t at = row * g.cols + col;
+    if (g.vec_in) {  // cols % 8 == 0: the eight elements are all inside
+        if constexpr (kIn == FP8_IN_F32) {
+            const float4 a = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(g.x) + at));
+            const float4 b = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(g.x) + at) + 1);
+            v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+            v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+        } else {
+            const uint4 a = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(g.x) + at));
+            const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if constexpr (kIn == FP8_IN_BF16) {
+                    v[2 * i] = __uint_as_float(w[i] << 16);
+                    v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+                } else {
+                    v[2 * i] = __half2float(__ushort_as_half(static_cast<uint16_t>(w[i] & 0xFFFFu)));
+                    v[2 * i + 1] = __half2float(__ushort_as_half(static_cast<uint16_t>(w[i] >> 16)));
+                }
+            }
+        }
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        if (col + i >= g.cols) {
+            v[i] = 0.0f;
+        } else if constexpr (kIn == FP8_IN_F32) {
+            v[i] = __ldg(static_cast<const float*>(g.x) + at + i);
+        } else {
+            const uint16_t e = __ldg(static_cast<const uint16_t*>(g.x) + at + i);
+            v[i] = kIn == FP8_IN_BF16 ? bf16_bits_to_float(e) : __half2float(__ushort_as_half(e));
+        }
+    }
+}
+
+// Eight bytes of row `row` from column `col` on.
+__device__ __forceinline__ void store8(uint8_t* out, const BlockQuantArgs& g, int vec, int64_t row, int64_t col,
+                                       uint32_t lo, uint32_t hi) {
+    if (row >= g.rows || col >= g.cols) return;
+    uint8_t* p = out + row * g.cols + col;
+    if (vec) {
+        *reinterpret_cast<uint2*>(p) = make_uint2(lo, hi);
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        if (col + i < g.cols) p[i] = static_cast<uint8_t>((i < 4 ? lo : hi) >> (8 * (i & 3)));
+}
+
+// kSquare: one scale per tile.  Otherwise kRow / kCol name the orientations wanted.
+template <int kIn, int kFmt, bool kRow, bool kCol, bool kSquare>
+__global__ void __launch_bounds__(kThreads, 2) block_quant_kernel(const __grid_constant__ BlockQuantArgs g) {
+    __shared__ float red[8][kB];
+    __shared__ float inv_col[kB];
+    constexpr float kMax = kFmt == 0 ? 448.0f : 57344.0f;
+    pdl_trigger();
+    pdl_wait();
+    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int64_t tr = blockIdx.x / g.tiles_c, tc = blockIdx.x - tr * g.tiles_c;
+    const int64_t row0 = tr * kB + ty, col0 = tc * kB + tx * kColsPer;
+
+    float v[kRowsPer][kColsPer];
+#pragma unroll
+    for (int r = 0; r < kRowsPer; ++r) load8<kIn>(g, row0 + 16 * r, col0, v[r]);
+
+    if constexpr (kSquare) {
+        float am = 0.0f;
+#pragma unroll
+        for (int r = 0; r < kRowsPer; ++r)
+#pragma unroll
+            for (int c = 0; c < kColsPer; ++c) am = fmaxf(am, fabsf(v[r][c]));
+        am = warp_max(am);
+        if (lane == 0) red[0][warp] = am;
+        __syncthreads();
+        am = red[0][0];
+#pragma unroll
+        for (int w = 1; w < 8; ++w) am = fmaxf(am, red[0][w]);
+        float s, inv;
+        block_step(am, kMax, s, inv);
+        if (threadIdx.x == 0) g.scale_row[tr * g.tiles_c + tc] = s;
+#pragma unroll
+        for (int r = 0; r < kRowsPer; ++r) {
+            float (&f)[kColsPer] = v[r];
+#pragma unroll
+            for (int c = 0; c < kColsPer; c += 2) mul2_rn(f[c], f[c + 1], inv);
+            store8(g.out_row, g, g.vec_row, row0 + 16 * r, col0, cvt_fp8x4<kFmt>(f[0], f[1], f[2], f[3]),
+                   cvt_fp8x4<kFmt>(f[4], f[5], f[6], f[7]));
+        }
+        return;
+    }
+
+    if constexpr (kRow) {
+        float mine = 0.0f;  // lane tx = r keeps the scale of row r
+#pragma unroll
+        for (int r = 0; r < kRowsPer; ++r) {
+            float am = 0.0f;
+#pragma unroll
+            for (int c = 0; c < kColsPer; ++c) am = fmaxf(am, fabsf(v[r][c]));
+#pragma unroll
+            for (int o = 8; o > 0; o >>= 1) am = fmaxf(am, __shfl_xor_sync(0xFFFFFFFFu, am, o));
+            float s, inv;
+            block_step(am, kMax, s, inv);
+            if (tx == r) mine = s;
+            float f[kColsPer];
+#pragma unroll
+            for (int c = 0; c < kColsPer; ++c) f[c] = v[r][c];
+#pragma unroll
+            for (int c = 0; c < kColsPer; c += 2) mul2_rn(f[c], f[c + 1], inv);
+            store8(g.out_row, g, g.vec_row, row0 + 16 * r, col0, cvt_fp8x4<kFmt>(f[0], f[1], f[2], f[3]),
+                   cvt_fp8x4<kFmt>(f[4], f[5], f[6], f[7]));
+        }
+        const int64_t row = row0 + 16 * tx;
+        if (tx < kRowsPer && row < g.rows) g.scale_row[tc * g.rows + row] = mine;
+    }
+
+    if constexpr (kCol) {
+        float am[kColsPer];
+#pragma unroll
+        for (int c = 0; c < kColsPer; ++c) {
+            am[c] = 0.0f;
+#pragma unroll
+            for (int r = 0; r < kRowsPer; ++r) am[c] = fmaxf(am[c], fabsf(v[r][c]));
+            am[c] = fmaxf(am[c], __shfl_xor_sync(0xFFFFFFFFu, am[c], 16));
+        }
+        if (lane < 16) {
+            float4* dst = reinterpret_cast<float4*>(&red[warp][tx * kColsPer]);
+            dst[0] = make_float4(am[0], am[1], am[2], am[3]);
+            dst[1] = make_float4(am[4], am[5], am[6], am[7]);
+        }
+        __syncthreads();
+        if (threadIdx.x < kB) {
+            const int c = threadIdx.x;
+            float a = red[0][c];
+#pragma unroll
+            for (int w = 1; w < 8; ++w) a = fmaxf(a, red[w][c]);
+            float s, inv;
+            block_step(a, kMax, s, inv);
+            inv_col[c] = inv;
+            const int64_t col = tc * kB + c;
+            if (col < g.cols) g.scale_col[tr * g.cols + col] = s;
+        }
+        __syncthreads();
+        const float4 i0 = *reinterpret_cast<const float4*>(&inv_col[tx * kColsPer]);
+        const float4 i1 = *reinterpret_cast<const float4*>(&inv_col[tx * kColsPer + 4]);
+#pragma unroll
+        for (int r = 0; r < kRowsPer; ++r) {
+            float f[kColsPer];
+#pragma unroll
+            for (int c = 0; c < kColsPer; ++c) f[c] = v[r][c];
+            mul2_pair_rn(f[0], f[1], i0.x, i0.y);
+            mul2_pair_rn(f[2], f[3], i0.z, i0.w);
+            mul2_pair_rn(f[4], f[5], i1.x, i1.y);
+            mul2_pair_rn(f[6], f[7], i1.z, i1.w);
+            store8(g.out_col, g, g.vec_col, row0 + 16 * r, col0, cvt_fp8x4<kFmt>(f[0], f[1], f[2], f[3]),
+                   cvt_fp8x4<kFmt>(f[4], f[5], f[6], f[7]));
+        }
+        if (g.colsum != nullptr) {
+            // column sums in a fixed order: a thread's rows, the two half-warps, the warps
+            float sum[kColsPer];
+#pragma unroll
+            for (int c = 0; c < kColsPer; ++c) {
+                sum[c] = 0.0f;
+#pragma unroll
+                for (int r = 0; r < kRowsPer; ++r) sum[c] += v[r][c];
+                sum[c] += __shfl_xor_sync(0xFFFFFFFFu, sum[c], 16);
+            }
+            // every thread is past its reads of `red` (the second barrier above)
+            if (lane < 16) {
+                float4* dst = reinterpret_cast<float4*>(&red[warp][tx * kColsPer]);
+                dst[0] = make_float4(sum[0], sum[1], sum[2], sum[3]);
+                dst[1] = make_float4(sum[4], sum[5], sum[6], sum[7]);
+            }
+            __syncthreads();
+            const int64_t col = tc * kB + threadIdx.x;
+            if (threadIdx.x < kB && col < g.cols) {
+                float a = red[0][threadIdx.x];
+#pragma unroll
+                for (int w = 1; w < 8; ++w) a += red[w][threadIdx.x];
+                g.colsum[tr * g.cols + col] = a;
+            }
+        }
+    }
+}
+
+template <int kIn, int kFmt>
+cudaError_t launch_fmt(const BlockQuantArgs& g, unsigned grid, bool square, cudaStream_t stream) {
+    if (square) return launch_ex(block_quant_kernel<kIn, kFmt, false, false, true>, dim3(grid), dim3(kThreads), 0, stream, 1, g);
+    if (g.out_row != nullptr && g.out_col != nullptr)
+        return launch_ex(block_quant_kernel<kIn, kFmt, true, true, false>, dim3(grid), dim3(kThreads), 0, stream, 1, g);
+    if (g.out_row != nullptr)
+        return launch_ex(block_quant_kernel<kIn, kFmt, true, false, false>, dim3(grid), dim3(kThreads), 0, stream, 1, g);
+    return launch_ex(block_quant_kernel<kIn, kFmt, false, true, false>, dim3(grid), dim3(kThreads), 0, stream, 1, g);
+}
+
+template <int kIn>
+cudaError_t launch_in(const BlockQuantArgs& g, fp8_fmt_t fmt, unsigned grid, bool square, cudaStream_t stream) {
+    return fmt == FP8_E4M3 ? launch_fmt<kIn, 0>(g, grid, square, stream) : launch_fmt<kIn, 1>(g, grid, square, stream);
+}
+
+}  // namespace
+
+int launch_block_quantize(const BlockQuantJob& j, cudaStream_t stream) {
+    if (j.rows <= 0 || j.cols <= 0) return FP8DSA_OK;
+    BlockQuantArgs g{};
+    g.x = j.x;
+    g.rows = j.rows;
+    g.cols = j.cols;
+    g.tiles_c = (j.cols + kB - 1) / kB;
+    const int64_t tiles_r = (j.rows + kB - 1) / kB;
+    if (tiles_r > 0x7FFFFFFF / g.tiles_c) return fail(FP8DSA_ERR_UNSUPPORTED, "block quantize: too many 128 x 128 tiles");
+    g.out_row = j.out_row;
+    g.scale_row = j.scale_row;
+    g.out_col = j.out_col;
+    g.scale_col = j.scale_col;
+    g.colsum = j.colsum;
+    g.vec_in = aligned16(j.x) && j.cols % 8 == 0;
+    g.vec_row = j.cols % 8 == 0 && (reinterpret_cast<uintptr_t>(j.out_row) & 7) == 0;
+    g.vec_col = j.cols % 8 == 0 && (reinterpret_cast<uintptr_t>(j.out_col) & 7) == 0;
+    const unsigned grid = static_cast<unsigned>(tiles_r * g.tiles_c);
+    const double elems = static_cast<double>(j.rows) * j.cols;
+    launch_begin(kKindQuantize, stream);
+    cudaError_t e;
+    switch (j.in_type) {
+        case FP8_IN_BF16: e = launch_in<FP8_IN_BF16>(g, j.fmt, grid, j.square, stream); break;
+        case FP8_IN_F16: e = launch_in<FP8_IN_F16>(g, j.fmt, grid, j.square, stream); break;
+        default: e = launch_in<FP8_IN_F32>(g, j.fmt, grid, j.square, stream); break;
+    }
+    if (e != cudaSuccess) return fail(FP8DSA_ERR_CUDA, std::string("block quantize launch: ") + cudaGetErrorString(e));
+    launch_end(kKindQuantize, stream,
+               elems * (in_type_bytes(j.in_type) + (j.out_row != nullptr ? 1 : 0) + (j.out_col != nullptr ? 1 : 0)));
+    return check_launch("block quantize kernel");
+}
+
+}  // namespace fp8dsa
+
+using namespace fp8dsa;
+
+extern "C" int fp8_quantize_block(const void* x, fp8_in_t in_type, int64_t rows, int64_t cols, fp8_fmt_t fmt,
+                                  uint8_t* out_row, float* scale_row, uint8_t* out_col, float* scale_col,
+                                  cudaStream_t stream) {
+    clear_error();
+    if (!valid_in_type(in_type)) return fail(FP8DSA_ERR_INVALID_ARG, "bad in_type");
+    if (!valid_fmt(fmt)) return fail(FP8DSA_ERR_INVALID_ARG, "fmt must be FP8_E4M3 or FP8_E5M2");
+    if (rows < 0 || cols < 0) return fail(FP8DSA_ERR_INVALID_ARG, "negative size");
+    if (rows > 0 && cols > 0) {
+        if (x == nullptr) return fail(FP8DSA_ERR_INVALID_ARG, "x is required");
+        if (out_row == nullptr && out_col == nullptr) return fail(FP8DSA_ERR_INVALID_ARG, "out_row or out_col is required");
+        if ((out_row == nullptr) != (scale_row == nullptr) || (out_col == nullptr) != (scale_col == nullptr))
+            return fail(FP8DSA_ERR_INVALID_ARG, "out_row and scale_row, out_col and scale_col go together");
+        if (reinterpret_cast<uintptr_t>(x) % in_type_bytes(in_type) != 0)
+            return fail(FP8DSA_ERR_UNSUPPORTED, "x must be aligned to its element size");
+        if ((reinterpret_cast<uintptr_t>(scale_row) & 3) != 0 || (reinterpret_cast<uintptr_t>(scale_col) & 3) != 0)
+            return fail(FP8DSA_ERR_UNSUPPORTED, "scales must be 4-byte aligned");
+    }
+    int rc = check_device();
+    if (rc) return rc;
+    BlockQuantJob j;
+    j.x = x;
+    j.in_type = in_type;
+    j.rows = rows;
+    j.cols = cols;
+    j.fmt = fmt;
+    j.out_row = out_row;
+    j.scale_row = scale_row;
+    j.out_col = out_col;
+    j.scale_col = scale_col;
+    return launch_block_quantize(j, stream);
+}
+
+extern "C" int fp8_quantize_block128(const void* x, fp8_in_t in_type, int64_t rows, int64_t cols, fp8_fmt_t fmt,
+                                     uint8_t* out, float* scale, cudaStream_t stream) {
+    clear_error();
+    if (!valid_in_type(in_type)) return fail(FP8DSA_ERR_INVALID_ARG, "bad in_type");
+    if (!valid_fmt(fmt)) return fail(FP8DSA_ERR_INVALID_ARG, "fmt must be FP8_E4M3 or FP8_E5M2");
+    if (rows < 0 || cols < 0) return fail(FP8DSA_ERR_INVALID_ARG, "negative size");
+    if (rows > 0 && cols > 0) {
+        if (x == nullptr || out == nullptr || scale == nullptr)
+            return fail(FP8DSA_ERR_INVALID_ARG, "x, out and scale are required");
+        if (reinterpret_cast<uintptr_t>(x) % in_type_bytes(in_type) != 0)
+            return fail(FP8DSA_ERR_UNSUPPORTED, "x must be aligned to its element size");
+        if ((reinterpret_cast<uintptr_t>(scale) & 3) != 0)
+            return fail(FP8DSA_ERR_UNSUPPORTED, "scale must be 4-byte aligned");
+    }
+    int rc = check_device();
+    if (rc) return rc;
+    BlockQuantJob j;
+    j.x = x;
+    j.in_type = in_type;
+    j.rows = rows;
+    j.cols = cols;
+    j.fmt = fmt;
+    j.out_row = out;
+    j.scale_row = scale;
+    j.square = true;
+    return launch_block_quantize(j, stream);
+}

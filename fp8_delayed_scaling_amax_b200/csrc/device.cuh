@@ -6,6 +6,7 @@
 
 #include <cuda.h>
 #include <cuda_runtime.h>
+#include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cstdint>
 
@@ -191,6 +192,28 @@ __device__ __forceinline__ void tc_fence_before_sync() {
 
 __device__ __forceinline__ void tc_fence_after_sync() {
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+}
+
+// UMMA shared-memory matrix descriptor: 128-byte swizzle, sm_100 descriptor version.
+__device__ __forceinline__ uint64_t smem_desc(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
+    uint64_t d = 0;
+    d |= static_cast<uint64_t>((saddr >> 4) & 0x3FFFu);
+    d |= static_cast<uint64_t>((lbo >> 4) & 0x3FFFu) << 16;
+    d |= static_cast<uint64_t>((sbo >> 4) & 0x3FFFu) << 32;
+    d |= static_cast<uint64_t>(1) << 46;  // descriptor version (sm_100)
+    d |= static_cast<uint64_t>(2) << 61;  // SWIZZLE_128B
+    return d;
+}
+
+// Warp-collective: each lane reads 16 consecutive 32-bit columns of its TMEM lane.
+__device__ __forceinline__ void tmem_load_16cols(uint32_t taddr, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32"
+        " {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr)
+        : "memory");
 }
 
 // Warp-collective: each lane reads 32 consecutive 32-bit columns of its TMEM lane.
@@ -445,6 +468,30 @@ __device__ __forceinline__ void ring_fold_deferred(float* st, int n, int idx, fl
     st[idx] = am;
     st[n] = fmaxf(__fdiv_rn(__fdiv_rn(peak, fp8_max), pow2_margin), 1e-12f);
     st[n + 2] = 0.0f;
+}
+
+__device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+// c = RN32(a * m + c), d = RN32(b * n + d) (fused, one rounding each) in one packed instruction.
+__device__ __forceinline__ void fma2_pair_rn(float& c, float& d, float a, float b, float m, float n) {
+    unsigned long long p, q, r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(p) : "f"(a), "f"(b));
+    asm("mov.b64 %0, {%1, %2};" : "=l"(q) : "f"(m), "f"(n));
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(c), "f"(d));
+    asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(r) : "l"(p), "l"(q));
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(c), "=f"(d) : "l"(r));
+}
+
+// a = RN32(a * m), b = RN32(b * n) in one packed instruction.
+__device__ __forceinline__ void mul2_pair_rn(float& a, float& b, float m, float n) {
+    unsigned long long p, q;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(p) : "f"(a), "f"(b));
+    asm("mov.b64 %0, {%1, %2};" : "=l"(q) : "f"(m), "f"(n));
+    asm("mul.rn.f32x2 %0, %0, %1;" : "+l"(p) : "l"(q));
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(p));
 }
 
 __device__ __forceinline__ float bf16_bits_to_float(uint32_t b) {

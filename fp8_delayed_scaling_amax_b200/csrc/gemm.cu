@@ -164,17 +164,6 @@ struct GemmArgs {
     WaitCtl wait;
 };
 
-// UMMA shared-memory matrix descriptor: 128-byte swizzle, sm_100 descriptor version.
-__device__ __forceinline__ uint64_t smem_desc(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
-    uint64_t d = 0;
-    d |= static_cast<uint64_t>((saddr >> 4) & 0x3FFFu);
-    d |= static_cast<uint64_t>((lbo >> 4) & 0x3FFFu) << 16;
-    d |= static_cast<uint64_t>((sbo >> 4) & 0x3FFFu) << 32;
-    d |= static_cast<uint64_t>(1) << 46;  // descriptor version (sm_100)
-    d |= static_cast<uint64_t>(2) << 61;  // SWIZZLE_128B
-    return d;
-}
-
 // Tile -> (problem, batch, tile row, tile column); grouped raster of FP8DSA_GEMM_GROUP_M tile rows per problem.
 __device__ __forceinline__ void decode_tile(int tile, const GemmArgs& g, int& pi, int& b, int& tm, int& tn) {
     constexpr int kGroupM = FP8DSA_GEMM_GROUP_M;
@@ -266,11 +255,6 @@ __device__ __forceinline__ bool named_barrier_or(int id, int nthreads, bool pred
         : "r"(pred ? 1u : 0u), "r"(id), "r"(nthreads)
         : "memory");
     return r != 0;
-}
-
-__device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
-    const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t*>(&v);
 }
 
 __device__ __forceinline__ float bias_value(const GemmProblem& P, int col, float bsc) {

@@ -154,6 +154,33 @@ int launch_colsum_finalize(const float* partial, int64_t tiles, int64_t cols, vo
 int launch_colsum_fp8(const uint8_t* g8, fp8_fmt_t fmt, int64_t rows, int64_t cols, const float* step,
                       float* partial, uint32_t* zero, int64_t zero_words, cudaStream_t stream);
 
+// Quantize with one scale per block of 128 (see block_quantize.cu); outputs not wanted are null.
+struct BlockQuantJob {
+    const void* x = nullptr;
+    fp8_in_t in_type = FP8_IN_BF16;
+    int64_t rows = 0, cols = 0;
+    fp8_fmt_t fmt = FP8_E4M3;
+    uint8_t* out_row = nullptr;   // [rows][cols], blocks of 1 x 128 (square: of 128 x 128)
+    float* scale_row = nullptr;   // [ceil(cols/128)][rows] (square: [ceil(rows/128)][ceil(cols/128)])
+    uint8_t* out_col = nullptr;   // [rows][cols], blocks of 128 x 1
+    float* scale_col = nullptr;   // [ceil(rows/128)][cols]
+    float* colsum = nullptr;      // [ceil(rows/128)][cols] column sums (with out_col only)
+    bool square = false;
+};
+int launch_block_quantize(const BlockQuantJob& job, cudaStream_t stream);
+
+// A product of block-scaled operands (see block_gemm.cu), arguments already validated.
+struct BlockGemmDesc {
+    const uint8_t* a;
+    const uint8_t* b;
+    int fmt_a, fmt_b, a_mn, b_mn;
+    int64_t m, n, k, lda, ldb, ldo, batch, stride_a, stride_b, stride_o;
+    fp8_block_scale_t sa, sb;
+    const void* bias;  // bf16 [n] or null
+    void* out;         // bf16
+};
+int block_gemm_launch(const BlockGemmDesc& d, cudaStream_t stream);
+
 // One GEMM of a launch, arguments already validated.
 struct GemmDesc {
     const uint8_t* a;

@@ -395,6 +395,64 @@ int linear_backward_fp8_saved_t(const void* g, const uint8_t* x8t, const uint8_t
                                 size_t workspace_bytes, void* grad_x, void* grad_w, void* grad_b,
                                 cudaStream_t stream);
 
+/* ---- One scale for each block of 128 ------------------------------------------------------
+ * The calls below hold FP8 tensors with an fp32 scale (step) for each block of 128 elements along
+ * the contraction instead of one per tensor, so an outlier costs one block's precision only and no
+ * history is needed.  A block's scale and bytes are the dynamic step's formula on that block:
+ *     s = max(RN32(max|x| / fp8_max), 1e-12),    q = q_fmt(RN32(x * RN32(1/s)))   (RN, saturating)
+ * NaN does not enter the maximum and becomes a NaN byte; a block that holds an infinity has an
+ * infinite scale and decodes to NaN throughout.  The last block of a row or column may be short.
+ * Not on the pages, which scale per tensor. */
+
+/* Quantize x (dev, rows x cols row-major, in_type, aligned to its element size) with
+ *   1 x 128 blocks along the rows:    out_row [rows][cols], scale_row [ceil(cols/128)][rows], and / or
+ *   128 x 1 blocks along the columns: out_col [rows][cols], scale_col [ceil(rows/128)][cols],
+ * both from one read of x.  An output and its scales are both given or both NULL.  The row form is a
+ * product's operand whose contraction runs along the rows (x and g of a linear layer), the column
+ * form one whose contraction runs down the columns (both operands of its weight gradient).
+ * Rows whose start and length are multiples of 8 elements and 16 bytes take the vector path. */
+int fp8_quantize_block(const void* x, fp8_in_t in_type, int64_t rows, int64_t cols, fp8_fmt_t fmt,
+                       uint8_t* out_row, float* scale_row, uint8_t* out_col, float* scale_col,
+                       cudaStream_t stream);
+
+/* Quantize x with 128 x 128 blocks (weights): out [rows][cols], scale
+ * [ceil(rows/128)][ceil(cols/128)].  The same bytes and scales serve the product along the rows
+ * and the product down the columns. */
+int fp8_quantize_block128(const void* x, fp8_in_t in_type, int64_t rows, int64_t cols, fp8_fmt_t fmt,
+                          uint8_t* out, float* scale, cudaStream_t stream);
+
+/* The scales of one operand of fp8_gemm_block: the scale of its row (A) or column (B) i in K block b
+ * (elements 128 b .. 128 b + 127 of the contraction) of batch c is
+ *     scale[(i / block_mn) * stride_mn + b * stride_kb + c * stride_batch],   block_mn = 1 or 128
+ * (strides in floats, >= 0).  With R rows, K columns and B(x) = ceil(x/128):
+ *   fp8_quantize_block rows,    contraction along the rows:    block_mn 1,   stride_mn 1,    stride_kb R
+ *   fp8_quantize_block columns, contraction down the columns:  block_mn 1,   stride_mn 1,    stride_kb K
+ *   fp8_quantize_block128,      contraction along the rows:    block_mn 128, stride_mn B(K), stride_kb 1
+ *   fp8_quantize_block128,      contraction down the columns:  block_mn 128, stride_mn 1,    stride_kb B(K) */
+typedef struct {
+    const float* scale; /* dev */
+    int block_mn;
+    int64_t stride_mn;
+    int64_t stride_kb;
+    int64_t stride_batch;
+} fp8_block_scale_t;
+
+/* FP8 x FP8 product of block-scaled operands:
+ *     out[c][i][j] = RN_bf16( sum_b RN32(sa(i,b) * sb(j,b)) * (sum_{k in block b} A[c][i][k] * B[c][k][j]) + bias[j] )
+ * each block's sum on the tensor cores (tcgen05.mma kind::f8f6f4), the blocks added in fp32 in
+ * order; where few output tiles have a long contraction, ranges of blocks are summed by CTAs of a
+ * cluster and added in range order (deterministic, no workspace).
+ *   a, b, formats, layouts, m, n, k, lda, ldb, ldo, batch and strides: as fp8_gemm (lda and ldb
+ *   multiples of 16, a and b 16-byte aligned, sizes below 2^31 - 256; stride 0 broadcasts an operand
+ *   -- give its scales stride_batch 0 as well).  The formats may differ.
+ *   scale_a, scale_b: host descriptors (see above).
+ *   bias: NULL or dev bf16[n].  out: dev bf16.  k == 0 writes the bias (or zeros). */
+int fp8_gemm_block(const uint8_t* a, const uint8_t* b, fp8_fmt_t fmt_a, fp8_fmt_t fmt_b,
+                   fp8_layout_t layout, int64_t m, int64_t n, int64_t k, int64_t lda, int64_t ldb,
+                   int64_t ldo, int64_t batch, int64_t stride_a, int64_t stride_b, int64_t stride_o,
+                   const fp8_block_scale_t* scale_a, const fp8_block_scale_t* scale_b,
+                   const void* bias, void* out, cudaStream_t stream);
+
 /* Device status word of the current device: 0, or a nonzero code a kernel set when a bounded
  * wait ran out (a pipeline stall instead of a hang).  Synchronises `stream`, reads the word
  * into *status (host) and clears it.  Not on the pages: added so no kernel can hang a GPU. */
