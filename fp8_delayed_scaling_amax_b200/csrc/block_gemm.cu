@@ -9,10 +9,9 @@
 // registers: acc = fma(d, sa * sb, acc).
 //
 // Structure (as the per-tensor GEMM, whose helpers it shares):
-//  * warp 0 = TMA producer, warp 1 = MMA issuer, 8 warps promote and write the output;
-//  * a stage holds one K block (128 bytes) of both operands; each K block goes to its own TMEM
-//    buffer (accumulate = 0 for its first MMA), handed over with one commit; the promotion of block
-//    b overlaps the MMAs of the blocks after it.  The tile's fp32 sums live in registers for the
+//  * warp 0 = TMA producer, warps 1 and 2 = MMA issuers, 8 warps promote and write the output;
+//  * a stage holds one K block (128 bytes) of both operands; each K block goes to a TMEM buffer of its
+//    own (accumulate = 0 for its first MMA), handed over with one commit; the promotion of block b overlaps the MMAs of the blocks after it.  The tile's fp32 sums live in registers for the
 //    whole K loop: 128 per thread for 256-wide tiles.
 //  * 256 x 256 tiles on CTA pairs (M = 256 MMA across two SMs, each SM loads half of B), or
 //    128 x 128 tiles on single CTAs when the pair tiles would leave most SMs idle; those may also
@@ -38,9 +37,24 @@ namespace {
 constexpr int kBM = 128;    // rows of a CTA's tile (TMEM lanes)
 constexpr int kBK = 128;    // K per stage: one scale block, one 128-byte swizzle row
 constexpr int kUmmaK = 32;
+constexpr int kIssuers = 2;  // MMA-issuing warps
 constexpr int kEpiWarps = 8;
 constexpr int kEpiThreads = 32 * kEpiWarps;
-constexpr int kThreads = 64 + kEpiThreads;
+
+// Promotion of a 256-wide tile needs more than the 168 registers that eleven warps leave a thread
+// (128 sums and 64 values in flight): its warps are two whole warpgroups that take over registers of
+// the first one (warp 3 only fills that).  384 threads launch with 168 each, 64,512 in all;
+// 128 x 56 + 256 x 224 = 64,512.  Nothing may spill: with all but 28 KB of an SM's L1 used as
+// shared memory, spilled registers go to L2 (8192^3 with 136 bytes of spills: 1357 against 1850 TFLOP/s).
+template <bool kRegSplit>
+struct Roles {
+    static constexpr int kFirstEpiWarp = kRegSplit ? 4 : 1 + kIssuers;
+    static constexpr int kThreads = 32 * kFirstEpiWarp + kEpiThreads;
+};
+constexpr int kOtherRegs = 56, kEpiRegs = 224;
+static_assert(128 * kOtherRegs + kEpiThreads * kEpiRegs <= Roles<true>::kThreads * 168, "registers a launch has");
+
+constexpr int kChunk = 32;  // columns per TMEM load
 constexpr int kOutBox = 64;                       // output columns per TMA store
 constexpr int kOutStageBytes = 32 * kOutBox * 2;  // one warp's 32 rows x 64 columns
 constexpr int kSmemLimit = 232448;
@@ -57,10 +71,11 @@ struct Cfg {
     static constexpr int kBStage = kBRows * kBK;
     static constexpr int kAccBufs = 512 / BN;               // TMEM buffers of one K block each
     static constexpr int kEpiCols = BN / (kEpiWarps / 4);   // columns per promotion warp
-    static constexpr int kOutBytes = kEpiWarps * kOutStageBytes;
-    static constexpr int kScaleBytes = kEpiWarps * 2 * kEpiCols * 4;  // per-column scales, double-buffered
+    static constexpr int kBoxes = kEpiCols / kOutBox;       // output boxes per promotion warp
+    static constexpr int kOutBytes = kEpiWarps * kBoxes * kOutStageBytes;
+    static_assert(3 * kEpiCols * 4 <= kOutBytes / kEpiWarps, "per-column scales (double-buffered) and bias lie in the output boxes");
     static constexpr int kBarBytes = 512;
-    static constexpr int kFixed = 1024 + kOutBytes + kScaleBytes + kBarBytes;
+    static constexpr int kFixed = kOutBytes + kBarBytes;
     static constexpr int kStagesFit = (kSmemLimit - kFixed) / (kAStage + kBStage);
     static constexpr int kStages = kStagesFit < kMaxStages ? kStagesFit : kMaxStages;
     static constexpr int kSmem = kFixed + kStages * (kAStage + kBStage);
@@ -113,20 +128,22 @@ __device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
 }
 
 template <int BN, bool kPair, bool kColScale, bool kSplit>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(Roles<kPair>::kThreads, 1)
     block_gemm_kernel(const __grid_constant__ CUtensorMap tma_a, const __grid_constant__ CUtensorMap tma_b,
                       const __grid_constant__ CUtensorMap tma_o, const __grid_constant__ BlockGemmArgs g) {
     using C = Cfg<BN, kPair>;
+    constexpr bool kRegSplit = kPair;
+    constexpr int kFirstEpiWarp = Roles<kRegSplit>::kFirstEpiWarp;
     constexpr int S = C::kStages;
     constexpr int kBufs = C::kAccBufs;
     static_assert(!(kPair && kSplit), "pairs do not split K");
-    extern __shared__ uint8_t smem_raw[];
-    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    // 1024-byte aligned by declaration (the swizzle's period): every address below is a constant, which
+    // the promotion warps' register budget needs
+    extern __shared__ __align__(1024) uint8_t smem[];
     uint8_t* sA = smem;
     uint8_t* sB = smem + S * C::kAStage;
     uint8_t* sOut = sB + S * C::kBStage;
-    float* sScale = reinterpret_cast<float*>(sOut + C::kOutBytes);
-    uint64_t* full = reinterpret_cast<uint64_t*>(sOut + C::kOutBytes + C::kScaleBytes);
+    uint64_t* full = reinterpret_cast<uint64_t*>(sOut + C::kOutBytes);
     uint64_t* empty = full + S;
     uint64_t* acc_full = empty + S;
     uint64_t* acc_empty = acc_full + kBufs;
@@ -152,7 +169,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(acc_full + a, 1);
             mbar_init(acc_empty + a, kEpiWarps * (kPair ? 2 : 1));  // one arrival per promotion warp
         }
-        mbar_init(drain, 1);
+        mbar_init(drain, kIssuers);
         *abort_flag = 0;
         fence_mbar_init();
         prefetch_tensormap(&tma_a);
@@ -179,129 +196,127 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int kb0 = kSplit ? static_cast<int>((static_cast<int64_t>(rank) * g.k_blocks) / g.splits) : 0;
     const int kb1 = kSplit ? static_cast<int>((static_cast<int64_t>(rank + 1) * g.k_blocks) / g.splits) : g.k_blocks;
 
-    float acc[C::kEpiCols];  // promotion warps: the tile's sums of this thread's row
-
-    if (warp == 0) {
-        // ------------------------------------------------------------------ TMA producer
-        if (lane == 0) {
-            int stage = 0;
-            uint32_t phase = 0;
-            uint32_t issued = 0, issued_parity = 0;
-            bool ok = true;
-            for (int t = unit; t < g.num_tiles && ok; t += units) {
-                int b, tm, tn;
-                decode_tile(t, g, b, tm, tn);
-                const int ba = g.a_batched ? b : 0;
-                const int bb = g.b_batched ? b : 0;
-                const int arow = tm * C::kTileM + (kPair ? static_cast<int>(rank) * kBM : 0);
-                const int brow = tn * BN + (kPair ? static_cast<int>(rank) * C::kBRows : 0);
-                for (int kb = kb0; kb < kb1; ++kb) {
-                    if (!mbar_wait_bounded(empty + stage, phase ^ 1u, g.wait, abort_flag, kStatusWaitProducer)) {
-                        ok = false;
-                        break;
-                    }
-                    if (leader) mbar_arrive_expect_tx(full + stage, C::kTxBytes);
-                    uint8_t* a_dst = sA + stage * C::kAStage;
-                    uint8_t* b_dst = sB + stage * C::kBStage;
-                    const int ac0 = g.a_mn ? arow : kb * kBK, ac1 = g.a_mn ? kb * kBK : arow;
-                    const int bc0 = g.b_mn ? brow : kb * kBK, bc1 = g.b_mn ? kb * kBK : brow;
-                    if constexpr (kPair) {
-                        const uint32_t fb = mapa_shared(smem_addr(full + stage), 0);
-                        tma_load_3d_pair(a_dst, &tma_a, fb, ac0, ac1, ba);
-                        tma_load_3d_pair(b_dst, &tma_b, fb, bc0, bc1, bb);
-                    } else {
-                        tma_load_3d(a_dst, &tma_a, full + stage, ac0, ac1, ba);
-                        tma_load_3d(b_dst, &tma_b, full + stage, bc0, bc1, bb);
-                    }
-                    issued |= 1u << stage;
-                    issued_parity = (issued_parity & ~(1u << stage)) | (phase << stage);
-                    if (++stage == S) {
-                        stage = 0;
-                        phase ^= 1u;
+    if (warp < kFirstEpiWarp) {
+        if constexpr (kRegSplit) regs_release<kOtherRegs>();
+        if (warp == 0) {
+            // ------------------------------------------------------------------ TMA producer
+            if (lane == 0) {
+                int stage = 0;
+                uint32_t phase = 0;
+                uint32_t issued = 0, issued_parity = 0;
+                bool ok = true;
+                for (int t = unit; t < g.num_tiles && ok; t += units) {
+                    int b, tm, tn;
+                    decode_tile(t, g, b, tm, tn);
+                    const int ba = g.a_batched ? b : 0;
+                    const int bb = g.b_batched ? b : 0;
+                    const int arow = tm * C::kTileM + (kPair ? static_cast<int>(rank) * kBM : 0);
+                    const int brow = tn * BN + (kPair ? static_cast<int>(rank) * C::kBRows : 0);
+                    for (int kb = kb0; kb < kb1; ++kb) {
+                        if (!mbar_wait_bounded(empty + stage, phase ^ 1u, g.wait, abort_flag, kStatusWaitProducer)) {
+                            ok = false;
+                            break;
+                        }
+                        if (leader) mbar_arrive_expect_tx(full + stage, C::kTxBytes);
+                        uint8_t* a_dst = sA + stage * C::kAStage;
+                        uint8_t* b_dst = sB + stage * C::kBStage;
+                        const int ac0 = g.a_mn ? arow : kb * kBK, ac1 = g.a_mn ? kb * kBK : arow;
+                        const int bc0 = g.b_mn ? brow : kb * kBK, bc1 = g.b_mn ? kb * kBK : brow;
+                        if constexpr (kPair) {
+                            const uint32_t fb = mapa_shared(smem_addr(full + stage), 0);
+                            tma_load_3d_pair(a_dst, &tma_a, fb, ac0, ac1, ba);
+                            tma_load_3d_pair(b_dst, &tma_b, fb, bc0, bc1, bb);
+                        } else {
+                            tma_load_3d(a_dst, &tma_a, full + stage, ac0, ac1, ba);
+                            tma_load_3d(b_dst, &tma_b, full + stage, bc0, bc1, bb);
+                        }
+                        issued |= 1u << stage;
+                        issued_parity = (issued_parity & ~(1u << stage)) | (phase << stage);
+                        if (++stage == S) {
+                            stage = 0;
+                            phase ^= 1u;
+                        }
                     }
                 }
+                if (!ok && leader) {
+                    // every copy in flight lands before the CTAs can exit
+                    for (int s = 0; s < S; ++s)
+                        if (issued & (1u << s))
+                            mbar_wait_bounded(full + s, (issued_parity >> s) & 1u, g.wait, nullptr, kStatusWaitDrain);
+                }
             }
-            if (!ok && leader) {
-                // every copy in flight lands before the CTAs can exit
-                for (int s = 0; s < S; ++s)
-                    if (issued & (1u << s))
-                        mbar_wait_bounded(full + s, (issued_parity >> s) & 1u, g.wait, nullptr, kStatusWaitDrain);
-            }
-        }
-        __syncwarp();
-    } else if (warp == 1) {
-        // ------------------------------------------------------------------ MMA issuer (leader)
-        if (leader) {
-            int stage = 0, buf = 0;
-            uint32_t phase = 0, buf_phase = 0;
-            bool ok = true;
-            for (int t = unit; t < g.num_tiles && ok; t += units) {
-                for (int kb = kb0; kb < kb1; ++kb) {
-                    const bool got = kPair ? mbar_wait_bounded_cluster(acc_empty + buf, buf_phase ^ 1u, g.wait,
-                                                                       abort_flag, kStatusWaitMma)
-                                           : mbar_wait_bounded(acc_empty + buf, buf_phase ^ 1u, g.wait, abort_flag,
-                                                               kStatusWaitMma);
-                    if (!got || !mbar_wait_bounded(full + stage, phase, g.wait, abort_flag, kStatusWaitMma)) {
-                        ok = false;
+            __syncwarp();
+        } else if (warp <= kIssuers) {
+            // ------------------------------------------------------------------ MMA issuers (leader)
+            // Two threads take the K blocks in turn, each with half of the TMEM buffers: one block's waits
+            // and commits (520 of about 970 cycles with a single issuer) run beside the other's MMAs.
+            if (leader && lane == 0) {
+                const int first = warp - 1;
+                const int64_t my_tiles = (g.num_tiles - 1 - unit) / units + 1;
+                const int64_t blocks = unit < g.num_tiles ? my_tiles * (kb1 - kb0) : 0;
+                int stage = first, buf = first;
+                uint32_t phase = 0, buf_phase = 0;
+                for (int64_t i = first; i < blocks; i += kIssuers) {
+                    if (!mbar_wait_bounded(acc_empty + buf, buf_phase ^ 1u, g.wait, abort_flag, kStatusWaitMma) ||
+                        !mbar_wait_bounded(full + stage, phase, g.wait, abort_flag, kStatusWaitMma))
                         break;
-                    }
                     tc_fence_after_sync();
-                    if (lane == 0) {
-                        const uint32_t a_base = smem_addr(sA + stage * C::kAStage);
-                        const uint32_t b_base = smem_addr(sB + stage * C::kBStage);
-                        const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(buf * BN);
+                    const uint32_t a_base = smem_addr(sA + stage * C::kAStage);
+                    const uint32_t b_base = smem_addr(sB + stage * C::kBStage);
+                    const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(buf * BN);
 #pragma unroll
-                        for (int kk = 0; kk < kBK / kUmmaK; ++kk) {
-                            // K-major: step 32 bytes along the swizzled row; MN-major: step 32 rows
-                            const uint64_t ad = g.a_mn ? smem_desc(a_base + kk * kUmmaK * 128, C::kAStage, 1024)
-                                                       : smem_desc(a_base + kk * kUmmaK, 16, 1024);
-                            const uint64_t bd = g.b_mn ? smem_desc(b_base + kk * kUmmaK * 128, C::kBStage, 1024)
-                                                       : smem_desc(b_base + kk * kUmmaK, 16, 1024);
-                            if constexpr (kPair)
-                                umma_f8f6f4_pair(d_tmem, ad, bd, g.idesc, kk != 0 ? 1u : 0u);
-                            else
-                                umma_f8f6f4(d_tmem, ad, bd, g.idesc, kk != 0 ? 1u : 0u);
-                        }
-                        if constexpr (kPair) {
-                            umma_commit_pair_multicast(empty + stage, 0x3);
-                            umma_commit_pair_multicast(acc_full + buf, 0x3);
-                        } else {
-                            umma_commit(empty + stage);
-                            umma_commit(acc_full + buf);
-                        }
+                    for (int kk = 0; kk < kBK / kUmmaK; ++kk) {
+                        // K-major: step 32 bytes along the swizzled row; MN-major: step 32 rows
+                        const uint64_t ad = g.a_mn ? smem_desc(a_base + kk * kUmmaK * 128, C::kAStage, 1024)
+                                                   : smem_desc(a_base + kk * kUmmaK, 16, 1024);
+                        const uint64_t bd = g.b_mn ? smem_desc(b_base + kk * kUmmaK * 128, C::kBStage, 1024)
+                                                   : smem_desc(b_base + kk * kUmmaK, 16, 1024);
+                        if constexpr (kPair)
+                            umma_f8f6f4_pair(d_tmem, ad, bd, g.idesc, kk != 0 ? 1u : 0u);
+                        else
+                            umma_f8f6f4(d_tmem, ad, bd, g.idesc, kk != 0 ? 1u : 0u);
                     }
-                    __syncwarp();
-                    if (++stage == S) {
-                        stage = 0;
+                    if constexpr (kPair) {
+                        umma_commit_pair_multicast(acc_full + buf, 0x3);
+                        umma_commit_pair_multicast(empty + stage, 0x3);
+                    } else {
+                        umma_commit(acc_full + buf);
+                        umma_commit(empty + stage);
+                    }
+                    stage += kIssuers;
+                    if (stage >= S) {
+                        stage -= S;
                         phase ^= 1u;
                     }
-                    if (++buf == kBufs) {
-                        buf = 0;
+                    buf += kIssuers;
+                    if (buf >= kBufs) {
+                        buf -= kBufs;
                         buf_phase ^= 1u;
                     }
                 }
-            }
-            // every MMA this thread issued must complete before TMEM is released
-            if (lane == 0) {
+                // every MMA the issuers sent off must complete before TMEM is released
                 if constexpr (kPair)
                     umma_commit_pair(drain);
                 else
                     umma_commit(drain);
                 mbar_wait_bounded(drain, 0, g.wait, nullptr, kStatusWaitDrain);
             }
+            __syncwarp();
         }
-        __syncwarp();
     } else {
         // ------------------------------------------------------------------ promotion and output
+        if constexpr (kRegSplit) regs_take<kEpiRegs>();
+        uint64_t acc[C::kEpiCols / 2];  // the tile's sums of this thread's row, two columns each
         // Warp w reads TMEM lanes 32 (w % 4) .. + 31, i.e. rows 32 (w % 4) + lane of the CTA's tile;
         // warps w and w + 4 split its columns.
-        const int ew = warp - 2;
+        const int ew = warp - kFirstEpiWarp;
         const int q = warp & 3;
         const int cbase = (ew >> 2) * C::kEpiCols;
-        uint8_t* my_stage = sOut + ew * kOutStageBytes;
-        float* my_scale = sScale + ew * 2 * C::kEpiCols;
+        const uint32_t tmem_mine = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(cbase);
+        uint8_t* my_stage = sOut + ew * C::kBoxes * kOutStageBytes;
+        float* my_scale = reinterpret_cast<float*>(my_stage);  // per-column scales share the output boxes
         const uint32_t acc_empty_leader = kPair ? mapa_shared(smem_addr(acc_empty), 0) : 0u;
-        int buf = 0, half = 0;
+        int buf = 0, flip = 0;
         uint32_t buf_phase = 0;
         bool ok = true;
         for (int t = unit; t < g.num_tiles && ok; t += units) {
@@ -311,88 +326,97 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int row = row0 + lane;
             const int col0 = tn * BN + cbase;
             // scales outside the matrix are never read: their products are never stored
-            const float* pa = row < g.m ? g.sa.p + static_cast<int64_t>(row >> g.sa.shift) * g.sa.s_mn + b * g.sa.s_b : nullptr;
-            constexpr int kPerLane = C::kEpiCols / 32;  // kColScale: columns col0 + lane + 32 i
-            const float* pb[kColScale ? kPerLane : 1];
-            if constexpr (kColScale) {
+            constexpr int kNb = kColScale ? C::kEpiCols / 32 : 1;  // kColScale: columns col0 + lane + 32 i
+            const int sb_col = col0 + (kColScale ? lane : 0);
+            const bool pa_in = row < g.m;
+            uint32_t pb_in = 0;
 #pragma unroll
-                for (int i = 0; i < kPerLane; ++i) {
-                    const int c = col0 + lane + 32 * i;
-                    pb[i] = c < g.n ? g.sb.p + static_cast<int64_t>(c >> g.sb.shift) * g.sb.s_mn + b * g.sb.s_b : nullptr;
-                }
-            } else {
-                pb[0] = col0 < g.n ? g.sb.p + static_cast<int64_t>(col0 >> g.sb.shift) * g.sb.s_mn + b * g.sb.s_b : nullptr;
-            }
-            float sa_next = 0.0f, sb_next[kColScale ? kPerLane : 1];
-            auto fetch = [&](int kb) {
-                sa_next = pa != nullptr ? __ldg(pa + kb * g.sa.s_kb) : 0.0f;
+            for (int i = 0; i < kNb; ++i) pb_in |= (sb_col + 32 * i < g.n ? 1u : 0u) << i;
+            const float* pa = g.sa.p + static_cast<int64_t>(row >> g.sa.shift) * g.sa.s_mn + b * g.sa.s_b + kb0 * g.sa.s_kb;
+            const float* pb = g.sb.p + static_cast<int64_t>(sb_col >> g.sb.shift) * g.sb.s_mn + b * g.sb.s_b + kb0 * g.sb.s_kb;
+            float sa_next = 0.0f, sb_next[kNb];
+            // the next K block's scales: loads that stay where they are written, a block ahead of their use
+            auto fetch = [&]() {
+                sa_next = pa_in ? ldg_pinned(pa) : 0.0f;
 #pragma unroll
-                for (int i = 0; i < (kColScale ? kPerLane : 1); ++i)
-                    sb_next[i] = pb[i] != nullptr ? __ldg(pb[i] + kb * g.sb.s_kb) : 0.0f;
+                for (int i = 0; i < kNb; ++i)
+                    sb_next[i] = (pb_in >> i & 1u) != 0 ? ldg_pinned(pb + i * 32 * g.sb.s_mn) : 0.0f;
+                pa += g.sa.s_kb;
+                pb += g.sb.s_kb;
             };
-            if (kb0 < kb1) fetch(kb0);
+            if (kb0 < kb1) fetch();
+            if constexpr (kColScale) {
+                if (lane == 0) bulk_wait_group_read<0>();  // the last tile's stores have read the box
+                __syncwarp();
+            }
 #pragma unroll
-            for (int c = 0; c < C::kEpiCols; ++c) acc[c] = 0.0f;
+            for (int c = 0; c < C::kEpiCols / 2; ++c) acc[c] = 0u;
 
             for (int kb = kb0; kb < kb1; ++kb) {
                 const float sa = sa_next;
-                float s = 0.0f;
-                float* cs = my_scale + half * C::kEpiCols;
-                half ^= 1;
+                uint64_t s2 = 0;  // RN32(sa * sb), twice
+                float* cs = my_scale + flip * C::kEpiCols;
+                flip ^= 1;
                 if constexpr (kColScale) {
                     // this half was last read two blocks ago, before this warp's last __syncwarp
 #pragma unroll
-                    for (int i = 0; i < kPerLane; ++i) cs[lane + 32 * i] = sb_next[i];
+                    for (int i = 0; i < kNb; ++i) cs[lane + 32 * i] = sb_next[i];
                     __syncwarp();
                 } else {
-                    s = sa * sb_next[0];
+                    const float s = __fmul_rn(sa, sb_next[0]);
+                    s2 = pack_f32x2(s, s);
                 }
-                if (kb + 1 < kb1) fetch(kb + 1);
+                if (kb + 1 < kb1) fetch();
                 if (!mbar_wait_bounded(acc_full + buf, buf_phase, g.wait, abort_flag, kStatusWaitEpilogue)) {
                     ok = false;
                 }
                 ok = __all_sync(0xFFFFFFFFu, ok);
                 if (!ok) break;
                 tc_fence_after_sync();
-                const uint32_t taddr = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(buf * BN + cbase);
-                uint32_t d[2][16];
-                tmem_load_16cols(taddr, d[0]);
+                const uint32_t taddr = tmem_mine + static_cast<uint32_t>(buf * BN);
+                // two 32-column loads in flight; a chunk's registers are loaded again as soon as it is added
+                uint32_t d[2][kChunk];
+                auto add = [&](int c, const uint32_t(&dc)[kChunk]) {
+                    if constexpr (kColScale) {
 #pragma unroll
-                for (int c = 0; c < C::kEpiCols / 16; ++c) {
-                    tmem_wait_ld();
-                    if (c + 1 < C::kEpiCols / 16) {
-                        tmem_load_16cols(taddr + 16 * (c + 1), d[(c + 1) & 1]);
+                        for (int e = 0; e < kChunk; e += 4) {
+                            // RN32(sa * sb), then one fma
+                            float4 f = *reinterpret_cast<const float4*>(cs + kChunk * c + e);
+                            const int i = (kChunk * c + e) / 2;
+                            mul2_rn(f.x, f.y, sa);
+                            mul2_rn(f.z, f.w, sa);
+                            fma_f32x2(acc[i], pack_b32x2(dc[e], dc[e + 1]), pack_f32x2(f.x, f.y));
+                            fma_f32x2(acc[i + 1], pack_b32x2(dc[e + 2], dc[e + 3]), pack_f32x2(f.z, f.w));
+                        }
                     } else {
+#pragma unroll
+                        for (int e = 0; e < kChunk; e += 2)
+                            fma_f32x2(acc[(kChunk * c + e) / 2], pack_b32x2(dc[e], dc[e + 1]), s2);
+                    }
+                };
+                constexpr int kChunks = C::kEpiCols / kChunk;
+                static_assert(kChunks % 2 == 0, "chunks in pairs");
+                tmem_load_32cols(taddr, d[0]);
+                tmem_load_32cols(taddr + kChunk, d[1]);
+#pragma unroll
+                for (int c = 0; c < kChunks; c += 2) {
+                    tmem_wait_ld();
+                    const bool last = c + 2 == kChunks;
+                    if (last) {
                         // the buffer is in registers: the MMAs of a later block may overwrite it
                         tc_fence_before_sync();
                         __syncwarp();
                         if (lane == 0) {
                             if (kPair && !leader)
-                                mbar_arrive_cluster(acc_empty_leader + static_cast<uint32_t>(buf * sizeof(uint64_t)));
+                                mbar_arrive_remote(acc_empty_leader + static_cast<uint32_t>(buf * sizeof(uint64_t)));
                             else
                                 mbar_arrive(acc_empty + buf);
                         }
                     }
-                    uint32_t(&dc)[16] = d[c & 1];
-                    if constexpr (kColScale) {
-#pragma unroll
-                        for (int e = 0; e < 16; e += 4) {
-                            const float4 f = *reinterpret_cast<const float4*>(cs + 16 * c + e);
-                            // RN32(sa * sb), then one fma
-                            float m0 = f.x, m1 = f.y, m2 = f.z, m3 = f.w;
-                            mul2_rn(m0, m1, sa);
-                            mul2_rn(m2, m3, sa);
-                            fma2_pair_rn(acc[16 * c + e], acc[16 * c + e + 1], __uint_as_float(dc[e]),
-                                         __uint_as_float(dc[e + 1]), m0, m1);
-                            fma2_pair_rn(acc[16 * c + e + 2], acc[16 * c + e + 3], __uint_as_float(dc[e + 2]),
-                                         __uint_as_float(dc[e + 3]), m2, m3);
-                        }
-                    } else {
-#pragma unroll
-                        for (int e = 0; e < 16; e += 2)
-                            fma2_pair_rn(acc[16 * c + e], acc[16 * c + e + 1], __uint_as_float(dc[e]),
-                                         __uint_as_float(dc[e + 1]), s, s);
-                    }
+                    add(c, d[0]);
+                    if (!last) tmem_load_32cols(taddr + kChunk * (c + 2), d[0]);
+                    add(c + 1, d[1]);
+                    if (!last) tmem_load_32cols(taddr + kChunk * (c + 3), d[1]);
                 }
                 if (++buf == kBufs) {
                     buf = 0;
@@ -403,49 +427,65 @@ __global__ void __launch_bounds__(kThreads, 1)
 
             if constexpr (!kSplit) {
                 // ---------------------------------------------------------- output of the whole tile
+                // Compact code: it runs once per tile, and instruction fetches are most of its time (with the
+                // bias and the direct stores inside the unrolled loop 3700 cycles a tile; moving them out
+                // took 2048 x 4096 x 1024 from 17.6 to 15.0 us).
+                if (lane == 0) bulk_wait_group_read<0>();  // the last tile's stores have read the boxes
+                __syncwarp();
+                if (g.bias != nullptr) {
+                    float* bs = reinterpret_cast<float*>(my_stage) + 2 * C::kEpiCols;  // clear of the scales
 #pragma unroll
-                for (int c = 0; c < C::kEpiCols; c += kOutBox) {
-                    const int colg = col0 + c;
-                    if (g.bias != nullptr) {
-                        float b_lo = 0.0f, b_hi = 0.0f;
-                        if (colg + lane < g.n) b_lo = bf16_bits_to_float(__ldg(g.bias + colg + lane));
-                        if (colg + 32 + lane < g.n) b_hi = bf16_bits_to_float(__ldg(g.bias + colg + 32 + lane));
+                    for (int i = 0; i < C::kEpiCols / 32; ++i) {
+                        const int col = col0 + lane + 32 * i;
+                        bs[lane + 32 * i] = col < g.n ? bf16_bits_to_float(__ldg(g.bias + col)) : 0.0f;
+                    }
+                    __syncwarp();
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) {
-                            acc[c + e] += __shfl_sync(0xFFFFFFFFu, b_lo, e);
-                            acc[c + 32 + e] += __shfl_sync(0xFFFFFFFFu, b_hi, e);
+                    for (int c = 0; c < C::kEpiCols; c += 4) {
+                        const ulonglong2 f = *reinterpret_cast<const ulonglong2*>(bs + c);
+                        acc[c / 2] = add_f32x2(acc[c / 2], f.x);
+                        acc[c / 2 + 1] = add_f32x2(acc[c / 2 + 1], f.y);
+                    }
+                    __syncwarp();
+                }
+#pragma unroll
+                for (int c = 0; c < C::kEpiCols; c += 8) {
+                    uint32_t w[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        float lo, hi;
+                        unpack_f32x2(acc[c / 2 + e], lo, hi);
+                        w[e] = pack_bf16x2(lo, hi);
+                    }
+                    // 128-byte swizzle: 16-byte chunk j of row r sits at chunk j ^ (r % 8)
+                    *reinterpret_cast<uint4*>(my_stage + (c / kOutBox) * kOutStageBytes + lane * 128 +
+                                              (((c % kOutBox / 8) ^ (lane & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+                }
+                if (g.tma_out) {
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0 && row0 < g.m) {
+#pragma unroll
+                        for (int i = 0; i < C::kBoxes; ++i)
+                            if (col0 + i * kOutBox < g.n)
+                                tma_store_3d(&tma_o, my_stage + i * kOutStageBytes, col0 + i * kOutBox, row0, b);
+                        bulk_commit_group();
+                    }
+                } else {
+                    // rows a tensor map cannot describe: each lane writes two columns of a row
+                    __syncwarp();
+                    for (int r = 0; r < 32 && row0 + r < g.m; ++r) {
+                        uint16_t* orow = g.out + static_cast<int64_t>(b) * g.stride_o + static_cast<int64_t>(row0 + r) * g.ldo;
+#pragma unroll
+                        for (int i = 0; i < C::kBoxes; ++i) {
+                            const int col = col0 + i * kOutBox + 2 * lane;
+                            const uint32_t v = *reinterpret_cast<const uint32_t*>(
+                                my_stage + i * kOutStageBytes + r * 128 + (((lane >> 2) ^ (r & 7)) << 4) + (lane & 3) * 4);
+                            if (col < g.n) orow[col] = static_cast<uint16_t>(v);
+                            if (col + 1 < g.n) orow[col + 1] = static_cast<uint16_t>(v >> 16);
                         }
                     }
-                    uint32_t packed[32];
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) packed[e] = pack_bf16x2(acc[c + 2 * e], acc[c + 2 * e + 1]);
-                    if (g.tma_out) {
-                        if (lane == 0) bulk_wait_group_read<0>();  // the box's last store has read it
-                        __syncwarp();
-                        // 128-byte swizzle: 16-byte chunk j of row r sits at chunk j ^ (r % 8)
-#pragma unroll
-                        for (int j = 0; j < 8; ++j)
-                            *reinterpret_cast<uint4*>(my_stage + lane * 128 + ((j ^ (lane & 7)) << 4)) =
-                                make_uint4(packed[4 * j], packed[4 * j + 1], packed[4 * j + 2], packed[4 * j + 3]);
-                        fence_proxy_async_smem();
-                        __syncwarp();
-                        if (lane == 0 && row0 < g.m && colg < g.n) {
-                            tma_store_3d(&tma_o, my_stage, colg, row0, b);
-                            bulk_commit_group();
-                        }
-                    } else if (row < g.m && colg < g.n) {
-                        uint16_t* orow = g.out + static_cast<int64_t>(b) * g.stride_o + static_cast<int64_t>(row) * g.ldo;
-                        if (g.vec_out && colg + kOutBox <= g.n) {
-                            uint4* dst = reinterpret_cast<uint4*>(orow + colg);
-#pragma unroll
-                            for (int v = 0; v < 8; ++v)
-                                dst[v] = make_uint4(packed[4 * v], packed[4 * v + 1], packed[4 * v + 2], packed[4 * v + 3]);
-                        } else {
-#pragma unroll
-                            for (int e = 0; e < kOutBox; ++e)
-                                if (colg + e < g.n) orow[colg + e] = static_cast<uint16_t>(packed[e >> 1] >> (16 * (e & 1)));
-                        }
-                    }
+                    __syncwarp();
                 }
             }
         }
@@ -454,10 +494,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             // (the last block's commit covers them); rows are kRedPad floats apart from a power of two
             if (ok) {
                 float* red = reinterpret_cast<float*>(smem);
-                float4* dst = reinterpret_cast<float4*>(red + (q * 32 + lane) * (BN + kRedPad) + cbase);
+                ulonglong2* dst = reinterpret_cast<ulonglong2*>(red + (q * 32 + lane) * (BN + kRedPad) + cbase);
 #pragma unroll
-                for (int c = 0; c < C::kEpiCols; c += 4)
-                    dst[c / 4] = make_float4(acc[c], acc[c + 1], acc[c + 2], acc[c + 3]);
+                for (int c = 0; c < C::kEpiCols; c += 4) dst[c / 4] = make_ulonglong2(acc[c / 2], acc[c / 2 + 1]);
             }
         }
         if (lane == 0) bulk_wait_group_all();
@@ -468,10 +507,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         // CTA r of the cluster adds rows [r * 128 / splits, ...) of all ranges, in range order, and
         // writes them.  Only after the second barrier may a CTA's shared memory go away.
         cluster_sync();
-        if (warp >= 2) {
+        if (warp >= kFirstEpiWarp) {
             int b, tm, tn;
             decode_tile(unit, g, b, tm, tn);
-            const int et = static_cast<int>(threadIdx.x) - 64;
+            const int et = static_cast<int>(threadIdx.x) - 32 * kFirstEpiWarp;
             const int r0 = (static_cast<int>(rank) * kBM) / g.splits, r1 = ((static_cast<int>(rank) + 1) * kBM) / g.splits;
             constexpr int kVec = BN / 8;  // eight columns per item
             for (int i = et; i < (r1 - r0) * kVec; i += kEpiThreads) {
@@ -552,7 +591,7 @@ cudaError_t kernel_setup(int* max_units_out) {
         at[0].val.clusterDim.y = 1;
         at[0].val.clusterDim.z = 1;
         cfg.gridDim = dim3(static_cast<unsigned>(2 * (sm_count() / 2)), 1, 1);
-        cfg.blockDim = dim3(kThreads, 1, 1);
+        cfg.blockDim = dim3(Roles<kPair>::kThreads, 1, 1);
         cfg.dynamicSmemBytes = C::kSmem;
         cfg.attrs = at;
         cfg.numAttrs = 1;
@@ -574,7 +613,8 @@ int launch_cfg(const CUtensorMap (&maps)[3], const BlockGemmArgs& g, cudaStream_
     // a split launch has one cluster per tile; the others walk the tiles
     const int group = kPair ? 2 : (kSplit ? g.splits : 1);
     const int64_t grid = static_cast<int64_t>(kSplit ? g.num_tiles : std::min(g.num_tiles, units)) * group;
-    e = launch_ex(block_gemm_kernel<BN, kPair, kColScale, kSplit>, dim3(static_cast<unsigned>(grid)), dim3(kThreads),
+    e = launch_ex(block_gemm_kernel<BN, kPair, kColScale, kSplit>, dim3(static_cast<unsigned>(grid)),
+                  dim3(Roles<kPair>::kThreads),
                   C::kSmem, stream, group, maps[0], maps[1], maps[2], g);
     if (e != cudaSuccess) return fail(FP8DSA_ERR_CUDA, std::string("block gemm launch: ") + cudaGetErrorString(e));
     return FP8DSA_OK;
