@@ -85,6 +85,15 @@ _SIGNATURES = {
     "fp8_gemm_block": (c_int, [_P, _P, c_int, c_int, c_int, c_int64, c_int64, c_int64, c_int64, c_int64, c_int64,
                                c_int64, c_int64, c_int64, c_int64, POINTER(fp8_block_scale_t),
                                POINTER(fp8_block_scale_t), _P, _P, _P]),
+    "linear_forward_fp8_block_workspace_size": (c_size_t, [c_int64, c_int64, c_int64]),
+    "linear_forward_fp8_block": (c_int, [_P, _P, c_int, _P, _P, c_int64, c_int64, c_int64, c_int, _P, _P, _P, _P, _P,
+                                         c_size_t, _P, _P]),
+    "linear_backward_fp8_block_workspace_size": (c_size_t, [c_int64, c_int64, c_int64]),
+    "linear_backward_fp8_block": (c_int, [_P, _P, _P, _P, _P, c_int64, c_int64, c_int64, c_int, c_int, c_int, c_int,
+                                          c_int, _P, c_size_t, _P, _P, _P, _P]),
+    "moe_forward_fp8_block_workspace_size": (c_size_t, [c_int64] * 5),
+    "moe_forward_fp8_block": (c_int, [_P, _P, _P, c_int64, c_int64, c_int64, c_int64, c_int64, c_int, _P, _P, _P, _P, _P,
+                                      c_size_t, _P, _P]),
     "fp8_get_device_status": (c_int, [_P, POINTER(c_int)]),
     "fp8_set_wait_timeout_ns": (c_int, [c_uint64]),
     "fp8_debug_stalled_wait": (c_int, [_P]),
@@ -380,6 +389,48 @@ def fp8_gemm_block(a, b, fmt_a, fmt_b, layout, m, n, k, lda, ldb, ldo, batch, st
         _ptr(a), _ptr(b), int(fmt_a), int(fmt_b), int(layout), int(m), int(n), int(k), int(lda), int(ldb), int(ldo),
         int(batch), int(stride_a), int(stride_b), int(stride_o), _block_scale(scale_a), _block_scale(scale_b),
         _ptr(bias), _ptr(out), _stream(stream)))
+
+
+def linear_forward_fp8_block_workspace_size(m, k, n) -> int:
+    return int(lib().linear_forward_fp8_block_workspace_size(int(m), int(k), int(n)))
+
+
+def linear_forward_fp8_block(x, w, w_is_fp8, w_scale, bias, m, k, n, fmt, w8_out, w_scale_out, x8c_out, x8c_scale_out,
+                             workspace, workspace_bytes, y, stream=None):
+    """Block-scaled linear forward; w8_out / x8c_out (with their scales) are what the backward reads."""
+    return _check("linear_forward_fp8_block", lib().linear_forward_fp8_block(
+        _ptr(x), _ptr(w), int(bool(w_is_fp8)), _ptr(w_scale), _ptr(bias), int(m), int(k), int(n), int(fmt),
+        _ptr(w8_out), _ptr(w_scale_out), _ptr(x8c_out), _ptr(x8c_scale_out), _ptr(workspace), int(workspace_bytes),
+        _ptr(y), _stream(stream)))
+
+
+def linear_backward_fp8_block_workspace_size(m, k, n) -> int:
+    return int(lib().linear_backward_fp8_block_workspace_size(int(m), int(k), int(n)))
+
+
+def linear_backward_fp8_block(g, x8c, x8c_scale, w8, w_scale, m, k, n, fmt_g, fmt, need_grad_x, need_grad_w, need_grad_b,
+                              workspace, workspace_bytes, grad_x, grad_w, grad_b, stream=None):
+    """Block-scaled linear backward from the operands linear_forward_fp8_block left."""
+    return _check("linear_backward_fp8_block", lib().linear_backward_fp8_block(
+        _ptr(g), _ptr(x8c), _ptr(x8c_scale), _ptr(w8), _ptr(w_scale), int(m), int(k), int(n), int(fmt_g), int(fmt),
+        int(bool(need_grad_x)), int(bool(need_grad_w)), int(bool(need_grad_b)), _ptr(workspace), int(workspace_bytes),
+        _ptr(grad_x), _ptr(grad_w), _ptr(grad_b), _stream(stream)))
+
+
+MOE_MAX_TOKENS, MOE_MAX_TOPK, MOE_MAX_EXPERTS = 64, 32, 1024
+
+
+def moe_forward_fp8_block_workspace_size(tokens, topk, experts, hidden, inter) -> int:
+    return int(lib().moe_forward_fp8_block_workspace_size(int(tokens), int(topk), int(experts), int(hidden), int(inter)))
+
+
+def moe_forward_fp8_block(x, ids, weights, tokens, topk, experts, hidden, inter, fmt, w13, w13_scale, w2, w2_scale,
+                          workspace, workspace_bytes, out, stream=None):
+    """Mixture-of-experts feed-forward layer for up to 64 tokens with block-scaled FP8 weights."""
+    return _check("moe_forward_fp8_block", lib().moe_forward_fp8_block(
+        _ptr(x), _ptr(ids), _ptr(weights), int(tokens), int(topk), int(experts), int(hidden), int(inter), int(fmt),
+        _ptr(w13), _ptr(w13_scale), _ptr(w2), _ptr(w2_scale), _ptr(workspace), int(workspace_bytes), _ptr(out),
+        _stream(stream)))
 
 
 def fp8_get_device_status(stream=None) -> int:

@@ -637,6 +637,7 @@ int block_gemm_launch(const BlockGemmDesc& d, cudaStream_t stream) {
         launch_end(kKindOther, stream, static_cast<double>(total) * 2);
         return check_launch("block fill kernel");
     }
+    if (d.m <= kStreamMaxRows && !d.a_mn) return block_stream_gemm(d, false, stream);
     auto tiles_of = [&](int64_t tm, int64_t tn) { return ((d.m + tm - 1) / tm) * ((d.n + tn - 1) / tn) * d.batch; };
     // Pair tiles unless they would keep at most half of the pairs busy.
     const bool pair = 4 * tiles_of(256, 256) > sm_count();

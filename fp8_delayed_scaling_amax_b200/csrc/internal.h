@@ -180,6 +180,10 @@ struct BlockGemmDesc {
     void* out;         // bf16
 };
 int block_gemm_launch(const BlockGemmDesc& d, cudaStream_t stream);
+// The same for m <= kStreamMaxRows and a K-major A (block_stream.cu): with x_is_bf16, A is bf16 (strides in
+// elements, sa unused) and quantized to fmt_a in 1 x 128 blocks on the way.
+constexpr int64_t kStreamMaxRows = 64;
+int block_stream_gemm(const BlockGemmDesc& d, bool x_is_bf16, cudaStream_t stream);
 
 // One GEMM of a launch, arguments already validated.
 struct GemmDesc {

@@ -453,6 +453,74 @@ int fp8_gemm_block(const uint8_t* a, const uint8_t* b, fp8_fmt_t fmt_a, fp8_fmt_
                    const fp8_block_scale_t* scale_a, const fp8_block_scale_t* scale_b,
                    const void* bias, void* out, cudaStream_t stream);
 
+/* Workspace bytes of linear_forward_fp8_block: x8 and w8 with their scales. */
+size_t linear_forward_fp8_block_workspace_size(int64_t m, int64_t k, int64_t n);
+
+/* Linear layer y = x w^T + bias with block scaling (the block-scaled counterpart of linear_forward_fp8):
+ *   x: dev bf16 [m][k], quantized in 1 x 128 blocks to `fmt`.
+ *   w: dev bf16 [n][k], quantized in 128 x 128 blocks, or with w_is_fp8 bytes in `fmt` (16-byte aligned)
+ *      with w_scale, dev fp32 [ceil(n/128)][ceil(k/128)].
+ *   bias: NULL or dev bf16[n].  y: dev bf16 [m][n].
+ *   For the backward: w8_out [n][k] and w_scale_out (bf16 w only; both or neither) receive the quantized
+ *   weight, x8c_out [m][k] and x8c_scale_out [ceil(m/128)][k] (both or neither) x in 128 x 1 blocks down
+ *   the tokens, in `fmt`; byte tensors 16-byte aligned.
+ *   workspace: dev, >= linear_forward_fp8_block_workspace_size(m, k, n) bytes, 256-byte aligned, no
+ *   initial contents.  k and n must be multiples of 16.
+ *   An fp8 weight with at most 64 rows of x and no x8c_out (decoding) is one launch. */
+int linear_forward_fp8_block(const void* x, const void* w, int w_is_fp8, const float* w_scale, const void* bias,
+                             int64_t m, int64_t k, int64_t n, fp8_fmt_t fmt, uint8_t* w8_out,
+                             float* w_scale_out, uint8_t* x8c_out, float* x8c_scale_out, void* workspace,
+                             size_t workspace_bytes, void* y, cudaStream_t stream);
+
+/* Workspace bytes of linear_backward_fp8_block: g in both forms, its scales and column sums. */
+size_t linear_backward_fp8_block_workspace_size(int64_t m, int64_t k, int64_t n);
+
+/* Backward of linear_forward_fp8_block from what it left:
+ *   g: dev bf16 [m][n], quantized to fmt_g in 1 x 128 blocks for grad_x and in 128 x 1 blocks for grad_w,
+ *   from one read; x8c, x8c_scale, w8, w_scale: the forward's x8c_out, x8c_scale_out and w8_out,
+ *   w_scale_out (or its fp8 w and w_scale), in `fmt`.
+ *       grad_x [m][k] = g8 . w8        grad_w [n][k] = g8c^T . x8c        grad_b [n] = RN_bf16(sum over rows of g)
+ *   dev bf16; need_grad_* select them (the others, and the operands only they use, may be NULL).
+ *   workspace: dev, >= linear_backward_fp8_block_workspace_size(m, k, n) bytes, 256-byte aligned, no
+ *   initial contents.  k and n must be multiples of 16, m may be any size. */
+int linear_backward_fp8_block(const void* g, const uint8_t* x8c, const float* x8c_scale, const uint8_t* w8,
+                              const float* w_scale, int64_t m, int64_t k, int64_t n, fp8_fmt_t fmt_g,
+                              fp8_fmt_t fmt, int need_grad_x, int need_grad_w, int need_grad_b,
+                              void* workspace, size_t workspace_bytes, void* grad_x, void* grad_w,
+                              void* grad_b, cudaStream_t stream);
+
+/* Limits of moe_forward_fp8_block. */
+#define FP8DSA_MOE_MAX_TOKENS 64
+#define FP8DSA_MOE_MAX_TOPK 32
+#define FP8DSA_MOE_MAX_EXPERTS 1024
+
+/* Workspace bytes of moe_forward_fp8_block (0 for sizes it refuses). */
+size_t moe_forward_fp8_block_workspace_size(int64_t tokens, int64_t topk, int64_t experts, int64_t hidden,
+                                            int64_t inter);
+
+/* Mixture-of-experts feed-forward layer for a few tokens (decoding), block-scaled FP8, two launches:
+ *   for every token t and slot s with 0 <= e = ids[t][s] < experts (other ids: the slot is skipped; an
+ *   expert may be named more than once, and a token without any valid slot gives a zero row):
+ *       (g, u) = q(x[t]) . w13[e]^T         q: fp8_quantize_block, 1 x 128 blocks, in fmt
+ *       h      = q( g / (1 + exp(-g)) * u ) formed and quantized from fp32
+ *   out[t] = RN_bf16( sum_s weights[t][s] * (h . w2[e]^T) )
+ * with the block scales applied and every sum in fp32; deterministic.
+ *   x: dev bf16 [tokens][hidden]; ids: dev int32 [tokens][topk]; weights: dev fp32 [tokens][topk].
+ *   w13: dev bytes in fmt [experts][2 inter][hidden], the gate's rows before the up rows, 16-byte aligned;
+ *   w13_scale: dev fp32 [experts][2][ceil(inter/128)][ceil(hidden/128)] (gate and up each have 128 x 128
+ *   blocks of their own: fp8_quantize_block128 of each [inter][hidden] half);
+ *   w2: dev bytes in fmt [experts][hidden][inter], 16-byte aligned;
+ *   w2_scale: dev fp32 [experts][ceil(hidden/128)][ceil(inter/128)].
+ *   tokens <= 64, topk <= 32, experts <= 1024; hidden and inter multiples of 16.
+ *   workspace: dev, >= moe_forward_fp8_block_workspace_size(...) bytes, 256-byte aligned, no initial
+ *   contents; calls that may overlap need one each.  out: dev bf16 [tokens][hidden].
+ * Only the weights of experts that are named are read.  Not on the pages. */
+int moe_forward_fp8_block(const void* x, const int* ids, const float* weights, int64_t tokens, int64_t topk,
+                          int64_t experts, int64_t hidden, int64_t inter, fp8_fmt_t fmt,
+                          const uint8_t* w13, const float* w13_scale, const uint8_t* w2,
+                          const float* w2_scale, void* workspace, size_t workspace_bytes, void* out,
+                          cudaStream_t stream);
+
 /* Device status word of the current device: 0, or a nonzero code a kernel set when a bounded
  * wait ran out (a pipeline stall instead of a hang).  Synchronises `stream`, reads the word
  * into *status (host) and clears it.  Not on the pages: added so no kernel can hang a GPU. */
