@@ -147,11 +147,23 @@ def _ptr(t):
     raise TypeError(f"expected a tensor, an int pointer or None, got {type(t)}")
 
 
+_raw_stream = None  # torch's current-stream lookup without a Stream object (0.2 us instead of 3.4)
+
+
 def _stream(stream):
     if stream is not None:
         return stream if isinstance(stream, int) else stream.cuda_stream
-    import torch
-    return torch.cuda.current_stream().cuda_stream
+    global _raw_stream
+    if _raw_stream is None:
+        import torch
+        current = torch.cuda.current_stream().cuda_stream  # initialises CUDA
+        get, device = getattr(torch._C, "_cuda_getCurrentRawStream", None), getattr(torch._C, "_cuda_getDevice", None)
+        if get is None or device is None:
+            _raw_stream = lambda: torch.cuda.current_stream().cuda_stream  # noqa: E731
+        else:
+            _raw_stream = lambda: get(device())  # noqa: E731
+        return current
+    return _raw_stream()
 
 
 def _ring(r):

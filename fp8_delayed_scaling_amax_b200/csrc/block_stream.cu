@@ -9,12 +9,14 @@
 //                 out[t] = RN_bf16( sum_s weight[t][s] * (W2[e] . hq) )
 //
 // Bound by reading the weight from HBM (every byte once per launch), for the smallest sizes by latency:
-//  * warp 0 streams 128 x 128 weight tiles by TMA into a ring of 16 KB slots; 100 to 190 KB per SM are in
-//    flight;
-//  * warps 2-5 build the token tiles (one K block each in turn, so their latencies overlap): FP8 rows are
-//    copied with their scales, bf16 rows are quantized on the way (1 x 128 blocks never leave a tile);
-//  * warp 1 issues the MMAs, one TMEM buffer per K block; warps 6-9 add the blocks with their scales in
-//    fp32 registers (a thread owns one weight row);
+//  * a ring of stages, each a 128 x 128 weight tile (gate and up: two), a token tile, its scales and a TMEM
+//    buffer: warp 0 streams the weights by TMA, warps 3-5 build the token tiles (FP8 rows are copied with
+//    their scales, bf16 rows quantized on the way: 1 x 128 blocks never leave a tile), warps 1 and 2
+//    issue the MMAs and warps 6-9 add the blocks with their scales in fp32 registers (a thread owns
+//    one weight row).  One commit per stage frees it for the producer and hands it to the adders.
+//    A single issuer with a ring and a commit each for weights, tokens and TMEM took 1200 to 1600
+//    cycles a unit (its waits 300 of them), more than a unit's bytes take from HBM.
+//  * two CTAs per SM for up to 16 tokens: 100 to 190 KB per SM are in flight;
 //  * the contraction is cut over a cluster of up to 8 CTAs; their fp32 sums meet in distributed shared
 //    memory and are added in range order, so results do not depend on timing and no workspace is needed.
 //  * experts: each CTA sorts the (token, slot) pairs by expert itself (a few hundred ids), so there is no
@@ -39,24 +41,32 @@ namespace {
 constexpr int kBM = 128;       // weight rows per tile (TMEM lanes)
 constexpr int kBK = 128;       // K per block
 constexpr int kUmmaK = 32;
-constexpr int kSlotBytes = kBM * kBK;
-constexpr int kBuilders = 4;
-constexpr int kFirstBuilder = 2, kFirstEpi = 6;
-constexpr int kThreads = 320;
-constexpr int kTmemCols = 256;   // two CTAs share an SM's 512 columns
-constexpr int kXSlots = 4;       // token tiles in flight
-constexpr int kMaxWSlots = 12;
-constexpr int kMaxBufs = 8;
-constexpr int kScaleSlots = 12;  // >= kXSlots + kMaxBufs: a slot is reused only after its block was added
+constexpr int kTileBytes = kBM * kBK;
+constexpr int kIssuers = 2;
+constexpr int kFirstBuilder = 1 + kIssuers;
+constexpr int kEpiThreads = 128;
+constexpr int kMaxStages = 12;
 constexpr int kBarBytes = 512;
 constexpr int kMaxSplit = 8;
 
 enum Mode : int { kDenseFp8 = 0, kDenseBf16 = 1, kUp = 2, kDown = 3 };
 
-// Two CTAs per SM (96 registers per thread, 112 KB each) where a thread's sums are few; the wide
-// instances keep 64 sums per thread and take an SM alone.
-constexpr int ctas_per_sm(int mode, int nmax) { return (mode == kUp ? 2 : 1) * nmax <= 32 ? 2 : 1; }
-constexpr int smem_budget(int ctas) { return ctas == 2 ? 112 * 1024 : 224 * 1024; }
+// Two CTAs per SM (96 registers per thread, 112 KB each) for up to 16 columns; the wide instances hold 64
+// sums per thread, or the outputs of 64 tokens, and take an SM alone.
+constexpr int ctas_per_sm(int nmax) { return nmax == 16 ? 2 : 1; }
+constexpr int smem_budget(int nmax) { return ctas_per_sm(nmax) == 2 ? 112 * 1024 : 224 * 1024; }
+constexpr int tmem_cols(int nmax) { return 512 / ctas_per_sm(nmax); }
+constexpr int builders(int nmax) { return nmax == 16 ? 3 : 5; }
+constexpr int threads_of(int nmax) { return 32 * (kFirstBuilder + builders(nmax)) + kEpiThreads; }
+// The roles that take units in turn wait for a stage's last use without having seen the uses between: with
+// at least as many stages as takers none of them can be a whole phase behind or ahead of a barrier.
+constexpr int min_stages(int nmax) { return builders(nmax); }
+static_assert(kIssuers <= 3 && min_stages(16) >= kIssuers, "issuers in turn");
+constexpr int tiles_of(int mode) { return mode == kUp ? 2 : 1; }
+constexpr int stage_bytes(int mode, int nmax) { return tiles_of(mode) * kTileBytes + nmax * kBK; }
+constexpr int max_stages(int mode, int nmax) {
+    return tmem_cols(nmax) / (tiles_of(mode) * nmax) < kMaxStages ? tmem_cols(nmax) / (tiles_of(mode) * nmax) : kMaxStages;
+}
 
 struct Scales {
     const float* p;
@@ -66,7 +76,7 @@ struct Scales {
 
 struct StreamArgs {
     int splits;       // CTAs per cluster
-    int w_slots;      // weight ring
+    int stages;       // ring
     int k_blocks;     // blocks of the contraction
     int row_tiles;    // 128-row tiles of the weight
     uint32_t idesc;   // without N
@@ -77,11 +87,12 @@ struct StreamArgs {
     const void* x;              // FP8 bytes or bf16
     int64_t ldx, x_batch;       // elements
     int x_vec;                  // rows are 16-byte aligned
-    int w_mn, w_batched;
+    int w_mn, w_batched, x_batched;
     Scales sw, sx;
     const uint16_t* bias;
     uint16_t* out;
     int64_t ldo, stride_o;
+    int out_vec;                // four outputs of a row are 8-byte aligned
     // experts
     const int* ids;
     const float* weights;
@@ -97,26 +108,20 @@ struct Entry {  // up to NMAX pairs of one expert
     uint16_t expert, start, n, pad;
 };
 
-__device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
-    float v;
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
-    return v;
+__device__ __forceinline__ void st_cluster_f32(uint32_t addr, float v) {
+    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
 }
-__device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
-    float4 v;
-    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-                 : "r"(addr)
-                 : "memory");
-    return v;
-}
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 
 // Pairs sorted by expert (stable), and the entries: runs of at most nmax pairs of one expert.
 struct Table {
     int* start;         // [experts] first sorted position (scratch before)
     uint16_t* id;       // [pairs] expert or 0xFFFF
     uint16_t* rank;     // [pairs] position among the expert's pairs
-    uint16_t* sorted;   // [pairs]
+    uint16_t* sorted;   // [pairs] the pair at a sorted position
+    uint16_t* token;    // [pairs] its token
+    float* weight;      // [pairs] its weight (second launch)
     Entry* entries;
     int* total;
 };
@@ -126,10 +131,10 @@ __host__ __device__ inline int max_entries(int pairs, int experts, int nmax) {
 }
 __host__ __device__ inline int table_bytes(int pairs, int experts, int nmax) {
     const int p8 = (pairs + 7) / 8 * 8;
-    return 16 + ((experts + 3) / 4 * 4) * 4 + 3 * p8 * 2 + max_entries(pairs, experts, nmax) * 8;
+    return 16 + ((experts + 3) / 4 * 4) * 4 + 4 * p8 * 2 + p8 * 4 + max_entries(pairs, experts, nmax) * 8;
 }
 
-__device__ __forceinline__ Table table_at(uint8_t* base, const StreamArgs& g, int nmax) {
+__device__ __forceinline__ Table table_at(uint8_t* base, const StreamArgs& g) {
     Table t;
     const int p8 = (g.pairs + 7) / 8 * 8;
     t.total = reinterpret_cast<int*>(base);
@@ -137,14 +142,52 @@ __device__ __forceinline__ Table table_at(uint8_t* base, const StreamArgs& g, in
     t.id = reinterpret_cast<uint16_t*>(t.start + (g.experts + 3) / 4 * 4);
     t.rank = t.id + p8;
     t.sorted = t.rank + p8;
-    t.entries = reinterpret_cast<Entry*>(t.sorted + p8);
-    (void)nmax;
+    t.token = t.sorted + p8;
+    t.weight = reinterpret_cast<float*>(t.token + p8);
+    t.entries = reinterpret_cast<Entry*>(t.weight + p8);
     return t;
 }
 
-// Whole CTA.  Deterministic: ranks follow the pairs' order.
+// Whole CTA.  Deterministic: ranks follow the pairs' order.  Ends with a barrier.
+template <bool kWeights, int kThreads>
 __device__ __forceinline__ void build_table(const Table& t, const StreamArgs& g, int nmax) {
     const int tid = threadIdx.x, lane = tid & 31;
+    auto place = [&](int pos, int p, float w) {
+        t.sorted[pos] = static_cast<uint16_t>(p);
+        t.token[pos] = static_cast<uint16_t>(p / g.topk);
+        if (kWeights) t.weight[pos] = w;
+    };
+    if (g.pairs <= 32) {
+        // one warp, in registers; entries in the order of their first pair
+        if (tid < 32) {
+            const int e0 = lane < g.pairs ? __ldg(g.ids + lane) : -1;
+            const float w = kWeights && lane < g.pairs ? __ldg(g.weights + lane) : 0.0f;
+            const bool valid = e0 >= 0 && e0 < g.experts;
+            const uint32_t mask = __match_any_sync(0xFFFFFFFFu, valid ? e0 : -1);
+            const uint32_t below = (1u << lane) - 1u;
+            const int rank = __popc(mask & below);
+            const bool leader = valid && rank % nmax == 0;  // the first pair of an entry
+            const uint32_t leaders = __ballot_sync(0xFFFFFFFFu, leader);
+            const int n = leader ? min(nmax, __popc(mask) - rank) : 0;
+            int start = n;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int v = __shfl_up_sync(0xFFFFFFFFu, start, o);
+                if (lane >= o) start += v;
+            }
+            start -= n;
+            if (leader)
+                t.entries[__popc(leaders & below)] =
+                    Entry{static_cast<uint16_t>(e0), static_cast<uint16_t>(start), static_cast<uint16_t>(n), 0};
+            // this pair's entry starts at the last leader of its expert up to itself
+            const uint32_t mine = leaders & mask & (below | (1u << lane));
+            const int from = __shfl_sync(0xFFFFFFFFu, start, valid ? 31 - __clz(mine) : lane);
+            if (valid) place(from + rank % nmax, lane, w);
+            if (lane == 0) *t.total = __popc(leaders);
+        }
+        __syncthreads();
+        return;
+    }
     for (int e = tid; e < g.experts; e += kThreads) t.start[e] = 0;
     for (int p = tid; p < g.pairs; p += kThreads) {
         const int e = __ldg(g.ids + p);
@@ -193,9 +236,13 @@ __device__ __forceinline__ void build_table(const Table& t, const StreamArgs& g,
     __syncthreads();
     for (int p = tid; p < g.pairs; p += kThreads) {
         const uint32_t e = t.id[p];
-        if (e != 0xFFFFu) t.sorted[t.start[e] + t.rank[p]] = static_cast<uint16_t>(p);
+        if (e != 0xFFFFu) place(t.start[e] + t.rank[p], p, kWeights ? __ldg(g.weights + p) : 0.0f);
     }
     __syncthreads();
+}
+
+__device__ __forceinline__ float block_step(float amax, int fmt) {
+    return fmaxf(__fdiv_rn(amax, fmt == 0 ? 448.0f : 57344.0f), 1e-12f);
 }
 
 // One K block of a bf16 row, 16 lanes per row (lane l16 holds elements 8 l16 ..): quantized into the
@@ -206,7 +253,7 @@ __device__ __forceinline__ float quant_row(uint8_t* tile, int j, int l16, const 
     float am = fmaxf(fabsf(__uint_as_float(m << 16)), fabsf(__uint_as_float(m & 0xFFFF0000u)));
 #pragma unroll
     for (int o = 8; o > 0; o >>= 1) am = fmaxf(am, __shfl_xor_sync(0xFFFFFFFFu, am, o));
-    const float s = fmaxf(__fdiv_rn(am, kFmt == 0 ? 448.0f : 57344.0f), 1e-12f);
+    const float s = block_step(am, kFmt);
     const float inv = __frcp_rn(s);
     float f[8];
 #pragma unroll
@@ -220,57 +267,96 @@ __device__ __forceinline__ float quant_row(uint8_t* tile, int j, int l16, const 
     return s;
 }
 
+// gate / (1 + exp(-gate)) * up in fp32
+__device__ __forceinline__ float gated(float gate, float up) { return __fdiv_rn(gate, 1.0f + expf(-gate)) * up; }
+
+// One warp: h of pair p in the 128 values of tile `tile`, from the ranges' sums (`ranges` parts `range_step`
+// floats apart, the up sums `up_step` behind the gate sums, column `j`), its block scale and its bytes.
+__device__ __forceinline__ void form_h(const StreamArgs& g, const float* recv, int ranges, int range_step, int up_step, int j,
+                                       int p, int tile, int lane) {
+    float v[2][4] = {};
+    for (int s = 0; s < ranges; ++s) {
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+            const float4 a = *reinterpret_cast<const float4*>(recv + s * range_step + t * up_step + j * kBM + 4 * lane);
+            v[t][0] += a.x;
+            v[t][1] += a.y;
+            v[t][2] += a.z;
+            v[t][3] += a.w;
+        }
+    }
+    const int i = tile * kBM + 4 * lane;  // inter is a multiple of 16: four rows are in or out
+    float h[4], am = 0.0f;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        h[e] = i < g.inter ? gated(v[0][e], v[1][e]) : 0.0f;
+        am = fmaxf(am, fabsf(h[e]));
+    }
+    am = warp_max(am);
+    const float s = block_step(am, g.fmt);
+    const float inv = __frcp_rn(s);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) h[e] = __fmul_rn(h[e], inv);
+    const uint32_t bytes = g.fmt == 0 ? cvt_fp8x4<0>(h[0], h[1], h[2], h[3]) : cvt_fp8x4<1>(h[0], h[1], h[2], h[3]);
+    if (i < g.inter) *reinterpret_cast<uint32_t*>(g.hq + static_cast<int64_t>(p) * g.inter + i) = bytes;
+    if (lane == 0) g.sh[static_cast<int64_t>(tile) * g.pairs + p] = s;
+}
+
+// Position in a CTA's sequence of units: K block `kb` of entry (experts) or tile `ent`.
+struct Cursor {
+    int ent, kb;
+    __device__ __forceinline__ void advance(int step, int k_blocks) {
+        kb += step;
+        while (kb >= k_blocks) {
+            kb -= k_blocks;
+            ++ent;
+        }
+    }
+};
+
 template <int kMode, int NMAX>
-__global__ void __launch_bounds__(kThreads, ctas_per_sm(kMode, NMAX))
-    block_stream_kernel(const __grid_constant__ CUtensorMap tma_w, const __grid_constant__ StreamArgs g) {
+__global__ void __launch_bounds__(threads_of(NMAX), ctas_per_sm(NMAX))
+    block_stream_kernel(const __grid_constant__ CUtensorMap tma_w, const __grid_constant__ CUtensorMap tma_x,
+                        const __grid_constant__ StreamArgs g) {
+    constexpr int kBuilders = builders(NMAX), kFirstEpi = kFirstBuilder + kBuilders, kThreads = threads_of(NMAX);
     constexpr bool kMoe = kMode == kUp || kMode == kDown;
     constexpr int kTiles = kMode == kUp ? 2 : 1;   // weight tiles per K block (gate and up)
-    constexpr int kBufCols = kTiles * NMAX;
-    constexpr int kBufs = kTmemCols / kBufCols < kMaxBufs ? kTmemCols / kBufCols : kMaxBufs;
-    static_assert(kXSlots + kBufs <= kScaleSlots, "scale ring");
+    constexpr int kStage = stage_bytes(kMode, NMAX);
+    constexpr int kCols = tmem_cols(NMAX);
     extern __shared__ __align__(1024) uint8_t smem[];
-    uint8_t* sX = smem;                                        // [kXSlots][NMAX][128]
-    uint8_t* sW = smem + kXSlots * NMAX * kBK;                 // [w_slots][128][128]
-    // behind the weight ring (its size is the launch's)
-    uint8_t* tail = sW + g.w_slots * kSlotBytes;
-    float* xs = reinterpret_cast<float*>(tail);                // [kScaleSlots][NMAX]
-    uint64_t* wfull = reinterpret_cast<uint64_t*>(tail + kScaleSlots * NMAX * 4);
-    uint64_t* wempty = wfull + kMaxWSlots;
-    uint64_t* sfull = wempty + kMaxWSlots;
-    uint64_t* xempty = sfull + kScaleSlots;
-    uint64_t* acc_full = xempty + kXSlots;
-    uint64_t* acc_empty = acc_full + kMaxBufs;
-    uint64_t* drain = acc_empty + kMaxBufs;
+    // stage st: weight tiles [128][128] each, then the token tile [NMAX][128]; behind the ring (its length
+    // is the launch's) the tokens' scales and the barriers
+    uint8_t* tail = smem + g.stages * kStage;
+    float* xs = reinterpret_cast<float*>(tail);                // [kMaxStages][NMAX]
+    uint64_t* full = reinterpret_cast<uint64_t*>(tail + kMaxStages * NMAX * 4);  // weights landed and tokens written
+    uint64_t* done = full + kMaxStages;                        // MMAs complete
+    uint64_t* added = done + kMaxStages;                       // sums and scales read
+    uint64_t* drain = added + kMaxStages;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-    static_assert((2 * kMaxWSlots + kScaleSlots + kXSlots + 2 * kMaxBufs + 1) * 8 + 8 <= kBarBytes, "barrier area");
+    static_assert((3 * kMaxStages + 1) * 8 + 8 <= kBarBytes, "barrier area");
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rank = static_cast<int>(cluster_ctarank());
-    const int item = static_cast<int>(blockIdx.x) / g.splits;
+    const int R = g.stages;
     if constexpr (kMode != kUp) pdl_trigger();
 
     if (threadIdx.x == 0) {
-        for (int i = 0; i < kMaxWSlots; ++i) {
-            mbar_init(wfull + i, 1);
-            mbar_init(wempty + i, 1);
+        for (int i = 0; i < R; ++i) {
+            mbar_init(full + i, 2);
+            mbar_init(done + i, 1);
+            mbar_init(added + i, 4);
         }
-        for (int i = 0; i < kScaleSlots; ++i) mbar_init(sfull + i, 1);
-        for (int i = 0; i < kXSlots; ++i) mbar_init(xempty + i, 1);
-        for (int i = 0; i < kMaxBufs; ++i) {
-            mbar_init(acc_full + i, 1);
-            mbar_init(acc_empty + i, 4);
-        }
-        mbar_init(drain, 1);
+        mbar_init(drain, kIssuers);
         *abort_flag = 0;
         fence_mbar_init();
         prefetch_tensormap(&tma_w);
     }
     if (warp == 1) {
-        tmem_alloc(tmem_slot, kTmemCols);
+        tmem_alloc(tmem_slot, kCols);
         tmem_relinquish();
     }
-    float* outacc = reinterpret_cast<float*>(smem + g.off_out);  // down: [tokens][128]
+    float* outacc = reinterpret_cast<float*>(smem + g.off_out);  // second launch: [tokens][128]
     if constexpr (kMode == kDown)
         for (int i = threadIdx.x; i < g.tokens * kBM; i += kThreads) outacc[i] = 0.0f;
     // The second expert launch reads only ids and weights before its wait: the first one has waited for
@@ -279,389 +365,471 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(kMode, NMAX))
     if constexpr (kMode == kUp) pdl_trigger();
     Table table{};
     if constexpr (kMoe) {
-        table = table_at(smem + g.off_table, g, NMAX);
-        build_table(table, g, NMAX);
+        table = table_at(smem + g.off_table, g);
+        build_table<kMode == kDown, kThreads>(table, g, NMAX);
     }
     tc_fence_before_sync();
     __syncthreads();
     tc_fence_after_sync();
     const uint32_t tmem_base = *tmem_slot;
 
-    // This CTA's work: units u0 .. u1 - 1, unit u = K block u % k_blocks of entry u / k_blocks.
-    int batch = 0, tile = 0;
-    int total = g.k_blocks;
-    bool idle = false;
+    // This CTA's units.  A cluster takes one item (a 128-row tile of the product, of one entry's gate and up,
+    // or of the second launch's outputs) and cuts its units over its CTAs; without clusters the first
+    // expert launch's CTAs walk all items.
+    const int cluster_id = static_cast<int>(blockIdx.x) / g.splits;
+    const int clusters = static_cast<int>(gridDim.x) / g.splits;
+    int items = 1, total = g.k_blocks;
     if constexpr (kMode == kUp) {
-        idle = item / g.row_tiles >= *table.total;  // fewer entries than the grid allows for
-        batch = item / g.row_tiles;                 // the entry
-        tile = item % g.row_tiles;
-    } else if constexpr (kMode == kDown) {
-        tile = item;
-        total = *table.total * g.k_blocks;
-    } else {
-        batch = item / g.row_tiles;
-        tile = item % g.row_tiles;
+        const int all = *table.total * g.row_tiles;
+        items = cluster_id < all ? (all - 1 - cluster_id) / clusters + 1 : 0;  // with clusters: one or none
     }
-    if (idle) total = 0;
+    if constexpr (kMode == kDown) total = *table.total * g.k_blocks;
     const int u0 = static_cast<int>((static_cast<int64_t>(rank) * total) / g.splits);
     const int u1 = static_cast<int>((static_cast<int64_t>(rank + 1) * total) / g.splits);
-    // entry of unit u (experts)
-    auto entry_of = [&](int u) { return table.entries[kMode == kUp ? batch : u / g.k_blocks]; };
-    auto block_of = [&](int u) { return kMode == kDown ? u % g.k_blocks : u; };
+    const int per_item = u1 - u0;       // with items > 1 the CTA has whole items
+    const int units = items * per_item;
+    // first cursor, and what a cursor stands for
+    auto first = [&](int skip) {
+        Cursor c{0, 0};
+        if constexpr (kMode == kDown) {
+            c.ent = u0 / g.k_blocks;
+            c.kb = u0 - c.ent * g.k_blocks;
+        } else {
+            c.kb = u0;
+        }
+        if (skip > 0) c.advance(skip, g.k_blocks);
+        return c;
+    };
+    // (first launch) item of cursor entry i: expert-major, so that CTAs side by side read one expert
+    auto item_of = [&](int ent) { return cluster_id + ent * clusters; };
+    auto tile_of = [&](int ent) { return kMode == kUp ? item_of(ent) % g.row_tiles : cluster_id % g.row_tiles; };
+    auto entry_at = [&](int ent) { return table.entries[kMode == kUp ? item_of(ent) / g.row_tiles : ent]; };
+    const int batch = kMoe ? 0 : cluster_id / g.row_tiles;
 
     if (warp == 0) {
         // ------------------------------------------------------------------ weights
         if (lane == 0) {
-            int slot = 0;
+            int st = 0, ent = -1, row = 0, e = 0;
             uint32_t phase = 0, issued = 0, parity = 0;
             bool ok = true;
-            for (int u = u0; u < u1 && ok; ++u) {
-                const int kb = block_of(u);
-                const int e = kMoe ? entry_of(u).expert : (g.w_batched ? batch : 0);
+            Cursor c = first(0);
+            for (int i = 0; i < units; ++i, c.advance(1, g.k_blocks)) {
+                if (c.ent != ent) {
+                    ent = c.ent;
+                    row = tile_of(ent) * kBM;
+                    e = kMoe ? entry_at(ent).expert : (g.w_batched ? batch : 0);
+                }
+                if (!mbar_wait_bounded(done + st, phase ^ 1u, g.wait, abort_flag, kStatusWaitProducer)) {
+                    ok = false;
+                    break;
+                }
+                mbar_arrive_expect_tx(full + st, kTiles * kTileBytes + (kMode == kDenseFp8 ? NMAX * kBK : 0));
 #pragma unroll
                 for (int t = 0; t < kTiles; ++t) {
-                    if (!mbar_wait_bounded(wempty + slot, phase ^ 1u, g.wait, abort_flag, kStatusWaitProducer)) {
-                        ok = false;
-                        break;
-                    }
-                    mbar_arrive_expect_tx(wfull + slot, kSlotBytes);
-                    const int row = tile * kBM + t * g.inter;  // up rows follow the gate rows
-                    tma_load_3d(sW + slot * kSlotBytes, &tma_w, wfull + slot, g.w_mn ? row : kb * kBK,
-                                g.w_mn ? kb * kBK : row, e);
-                    issued |= 1u << slot;
-                    parity = (parity & ~(1u << slot)) | (phase << slot);
-                    if (++slot == g.w_slots) {
-                        slot = 0;
-                        phase ^= 1u;
-                    }
+                    const int r = row + t * g.inter;  // up rows follow the gate rows
+                    tma_load_3d(smem + st * kStage + t * kTileBytes, &tma_w, full + st, g.w_mn ? r : c.kb * kBK,
+                                g.w_mn ? c.kb * kBK : r, e);
+                }
+                if constexpr (kMode == kDenseFp8)  // FP8 rows come by TMA (rows from ncols on are zeros)
+                    tma_load_3d(smem + st * kStage + kTiles * kTileBytes, &tma_x, full + st, c.kb * kBK, 0, g.x_batched ? batch : 0);
+                issued |= 1u << st;
+                parity = (parity & ~(1u << st)) | (phase << st);
+                if (++st == R) {
+                    st = 0;
+                    phase ^= 1u;
                 }
             }
-            if (!ok)  // every copy in flight lands before the CTA can exit
-                for (int s = 0; s < g.w_slots; ++s)
-                    if (issued & (1u << s))
-                        mbar_wait_bounded(wfull + s, (parity >> s) & 1u, g.wait, nullptr, kStatusWaitDrain);
+            // Every copy in flight lands before the CTA can exit.  (A stage's barrier also counts its token
+            // tile, which may never come: one wait that runs out has covered the other copies as well.)
+            if (!ok)
+                for (int s = 0; s < R; ++s)
+                    if ((issued & (1u << s)) != 0 &&
+                        !mbar_wait_bounded(full + s, (parity >> s) & 1u, g.wait, nullptr, kStatusWaitDrain))
+                        break;
         }
         __syncwarp();
-    } else if (warp == 1) {
-        // ------------------------------------------------------------------ MMA issuer
+        cluster_arrive();
+        cluster_wait();
+    } else if (warp <= kIssuers) {
+        // ------------------------------------------------------------------ MMA issuers: units in turn
         if (lane == 0) {
-            int slot = 0, xslot = 0, sslot = 0, buf = 0;
-            uint32_t wphase = 0, sphase = 0, bphase = 0;
-            for (int u = u0; u < u1; ++u) {
-                const int n = kMoe ? static_cast<int>(entry_of(u).n) : g.ncols;
-                const uint32_t idesc = g.idesc | (static_cast<uint32_t>((n + 15) / 16 * 2) << 17);  // N = n up to a multiple of 16
-                if (!mbar_wait_bounded(acc_empty + buf, bphase ^ 1u, g.wait, abort_flag, kStatusWaitMma) ||
-                    !mbar_wait_bounded(sfull + sslot, sphase, g.wait, abort_flag, kStatusWaitMma))
+            const int h = warp - 1;
+            int st = h, ent = -1;
+            uint32_t phase = 0, idesc = g.idesc;
+            Cursor c = first(h);
+            for (int i = h; i < units; i += kIssuers, c.advance(kIssuers, g.k_blocks)) {
+                if (c.ent != ent) {
+                    ent = c.ent;
+                    const int n = kMoe ? static_cast<int>(entry_at(ent).n) : g.ncols;
+                    idesc = g.idesc | (static_cast<uint32_t>((n + 15) / 16 * 2) << 17);  // N = n up to a multiple of 16
+                }
+                if (!mbar_wait_bounded(added + st, phase ^ 1u, g.wait, abort_flag, kStatusWaitMma) ||
+                    !mbar_wait_bounded(full + st, phase, g.wait, abort_flag, kStatusWaitMma))
                     break;
-                bool ok = true;
+                tc_fence_after_sync();
+                const uint32_t a_base = smem_addr(smem) + static_cast<uint32_t>(st * kStage);
+                const uint32_t b_base = a_base + kTiles * kTileBytes;
+                const uint32_t d = tmem_base + static_cast<uint32_t>(st * kTiles * NMAX);
 #pragma unroll
                 for (int t = 0; t < kTiles; ++t) {
-                    if (!mbar_wait_bounded(wfull + slot, wphase, g.wait, abort_flag, kStatusWaitMma)) {
-                        ok = false;
-                        break;
-                    }
-                    tc_fence_after_sync();
-                    const uint32_t a_base = smem_addr(sW + slot * kSlotBytes);
-                    const uint32_t b_base = smem_addr(sX + xslot * NMAX * kBK);
-                    const uint32_t d = tmem_base + static_cast<uint32_t>(buf * kBufCols + t * NMAX);
 #pragma unroll
                     for (int kk = 0; kk < kBK / kUmmaK; ++kk) {
-                        const uint64_t ad = g.w_mn ? smem_desc(a_base + kk * kUmmaK * 128, kSlotBytes, 1024)
-                                                   : smem_desc(a_base + kk * kUmmaK, 16, 1024);
-                        umma_f8f6f4(d, ad, smem_desc(b_base + kk * kUmmaK, 16, 1024), idesc, kk != 0 ? 1u : 0u);
-                    }
-                    umma_commit(wempty + slot);
-                    if (++slot == g.w_slots) {
-                        slot = 0;
-                        wphase ^= 1u;
+                        const uint32_t a = a_base + t * kTileBytes;
+                        const uint64_t ad = g.w_mn ? smem_desc(a + kk * kUmmaK * 128, kTileBytes, 1024)
+                                                   : smem_desc(a + kk * kUmmaK, 16, 1024);
+                        umma_f8f6f4(d + t * NMAX, ad, smem_desc(b_base + kk * kUmmaK, 16, 1024), idesc, kk != 0 ? 1u : 0u);
                     }
                 }
-                if (!ok) break;
-                umma_commit(xempty + xslot);
-                umma_commit(acc_full + buf);
-                if (++xslot == kXSlots) xslot = 0;
-                if (++sslot == kScaleSlots) {
-                    sslot = 0;
-                    sphase ^= 1u;
-                }
-                if (++buf == kBufs) {
-                    buf = 0;
-                    bphase ^= 1u;
+                umma_commit(done + st);
+                st += kIssuers;
+                if (st >= R) {
+                    st -= R;
+                    phase ^= 1u;
                 }
             }
-            // every MMA this thread issued must complete before TMEM is released
+            // every MMA the issuers sent off must complete before TMEM is released
             umma_commit(drain);
             mbar_wait_bounded(drain, 0, g.wait, nullptr, kStatusWaitDrain);
         }
         __syncwarp();
+        cluster_arrive();
+        cluster_wait();
     } else if (warp < kFirstEpi) {
         // ------------------------------------------------------------------ token tiles
-        // Warp w builds blocks w - 2, w + 2, ...: four blocks' loads are under way at once.  Columns from n
-        // on are left as they are: a column of the product depends on its own token only.
+        // The builders take the units in turn.  Columns from n on are left as they are: a column of the
+        // product depends on its own token only.  The next batch of rows is loaded before this one is
+        // converted and before a stage is waited for.
         if constexpr (kMode == kDown) pdl_wait();  // hq is the first launch's
-        for (int i = warp - kFirstBuilder; u0 + i < u1; i += kBuilders) {
-            const int u = u0 + i, kb = block_of(u);
-            const int xslot = i % kXSlots, sslot = i % kScaleSlots;
-            bool ok = mbar_wait_bounded(xempty + xslot, ((i / kXSlots) & 1) ^ 1u, g.wait, abort_flag, kStatusWaitProducer);
+        constexpr bool kQuant = kMode == kDenseBf16 || kMode == kUp;
+        // quantizing: 16 lanes per row, 8 elements each; copying: 8 lanes per row, 16 bytes each (a product's
+        // FP8 rows come by TMA: only their scales are copied)
+        constexpr int kRowsAtOnce = kQuant ? 2 : 4;
+        constexpr int kUnroll = kMode == kDenseFp8 ? 1 : kQuant ? 4 : NMAX / 4;
+        static_assert(kQuant || kMode == kDenseFp8 || NMAX <= 32, "a copied tile is one batch");
+        constexpr int kBatch = kMode == kDenseFp8 ? NMAX : kRowsAtOnce * kUnroll;
+        constexpr int kScales = kQuant ? 1 : (NMAX + 31) / 32;  // copying: scales per lane
+        const int lrow = kQuant ? lane >> 4 : lane >> 3;        // row within kRowsAtOnce
+        const int lcol = kQuant ? (lane & 15) * 8 : (lane & 7) * 16;
+        const int64_t klen = kMode == kUp ? g.hidden : kMode == kDown ? g.inter : g.k;
+        struct Batch {
+            uint4 v[kUnroll];
+        } cur, nxt;
+        float sc_cur[kScales], sc_nxt[kScales];
+        auto columns = [&](int ent) { return kMoe ? static_cast<int>(entry_at(ent).n) : g.ncols; };
+        auto load = [&](Cursor c, int n, int j0, Batch& out, float (&scale)[kScales]) {
+            const int pos = kMoe ? static_cast<int>(entry_at(c.ent).start) : 0;
+            const int64_t col = static_cast<int64_t>(c.kb) * kBK + lcol;
+#pragma unroll
+            for (int r = 0; r < (kMode == kDenseFp8 ? 0 : kUnroll); ++r) {
+                const int j = j0 + kRowsAtOnce * r + lrow;
+                out.v[r] = make_uint4(0u, 0u, 0u, 0u);
+                if (j >= n || col >= klen) continue;
+                if constexpr (kQuant) {
+                    const uint16_t* row = static_cast<const uint16_t*>(g.x) +
+                                          (kMode == kUp ? table.token[pos + j] * g.ldx : batch * g.x_batch + j * g.ldx);
+                    if (g.x_vec) {  // k % 8 == 0: the eight elements are all inside
+                        out.v[r] = __ldg(reinterpret_cast<const uint4*>(row + col));
+                    } else {
+                        uint32_t w[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+                        for (int e = 0; e < 8; ++e)
+                            if (col + e < klen) w[e >> 1] |= static_cast<uint32_t>(__ldg(row + col + e)) << (16 * (e & 1));
+                        out.v[r] = make_uint4(w[0], w[1], w[2], w[3]);
+                    }
+                } else if constexpr (kMode == kDown) {  // inter is a multiple of 16
+                    out.v[r] = __ldcg(reinterpret_cast<const uint4*>(g.hq + static_cast<int64_t>(table.sorted[pos + j]) * g.inter + col));
+                }
+            }
+            if (!kQuant && j0 == 0) {
+#pragma unroll
+                for (int q = 0; q < kScales; ++q) {
+                    const int j = lane + 32 * q;
+                    scale[q] = 0.0f;
+                    if (j < n)
+                        scale[q] = kMode == kDown
+                                       ? __ldcg(g.sh + static_cast<int64_t>(c.kb) * g.pairs + table.sorted[pos + j])
+                                       : __ldg(g.sx.p + static_cast<int64_t>(j >> g.sx.shift) * g.sx.s_mn + c.kb * g.sx.s_kb +
+                                               batch * g.sx.s_b);
+                }
+            }
+        };
+        int i = warp - kFirstBuilder, st = i % R, n = 0;
+        uint32_t phase = static_cast<uint32_t>(i / R) & 1u;
+        Cursor c = first(i);
+        if (i < units) {
+            n = columns(c.ent);
+            load(c, n, 0, cur, sc_cur);
+        }
+        while (i < units) {
+            Cursor cn = c;
+            cn.advance(kBuilders, g.k_blocks);
+            const bool more = i + kBuilders < units;
+            const int nn = more ? (cn.ent == c.ent ? n : columns(cn.ent)) : 0;
+            bool ok = mbar_wait_bounded(added + st, phase ^ 1u, g.wait, abort_flag, kStatusWaitProducer);
             ok = __all_sync(0xFFFFFFFFu, ok);
             if (!ok) break;
-            uint8_t* dst = sX + xslot * NMAX * kBK;
-            float* sc = xs + sslot * NMAX;
-            int n = g.ncols;
-            const uint16_t* pairs = nullptr;
-            if constexpr (kMoe) {
-                const Entry en = entry_of(u);
-                n = en.n;
-                pairs = table.sorted + en.start;
-            }
-            if constexpr (kMode == kDenseBf16 || kMode == kUp) {
-                const int half = lane >> 4, l16 = lane & 15;
-                const int64_t klen = kMode == kUp ? g.hidden : g.k;
-                const int64_t col = static_cast<int64_t>(kb) * kBK + 8 * l16;
-                constexpr int kUnroll = 4;  // row pairs whose loads are under way together
-                for (int j0 = 0; j0 < n; j0 += 2 * kUnroll) {
-                    uint32_t w[kUnroll][4];
+            uint8_t* dst = smem + st * kStage + kTiles * kTileBytes;
+            float* sc = xs + st * NMAX;
+            for (int j0 = 0; j0 < n; j0 += kBatch) {
+                if (!kQuant && j0 == 0) {
 #pragma unroll
-                    for (int r = 0; r < kUnroll; ++r) {
-                        const int j = j0 + 2 * r + half;
+                    for (int q = 0; q < kScales; ++q)
+                        if (lane + 32 * q < n) sc[lane + 32 * q] = sc_cur[q];
+                }
+                if (j0 + kBatch < n)
+                    load(c, n, j0 + kBatch, nxt, sc_nxt);
+                else if (more)
+                    load(cn, nn, 0, nxt, sc_nxt);
 #pragma unroll
-                        for (int v = 0; v < 4; ++v) w[r][v] = 0u;
-                        if (j < n && col < klen) {
-                            const uint16_t* row =
-                                static_cast<const uint16_t*>(g.x) +
-                                (kMode == kUp ? static_cast<int64_t>(pairs[j] / g.topk) * g.ldx : batch * g.x_batch + j * g.ldx);
-                            if (g.x_vec) {  // k % 8 == 0: the eight elements are all inside
-                                const uint4 a = __ldg(reinterpret_cast<const uint4*>(row + col));
-                                w[r][0] = a.x;
-                                w[r][1] = a.y;
-                                w[r][2] = a.z;
-                                w[r][3] = a.w;
-                            } else {
-#pragma unroll
-                                for (int v = 0; v < 8; ++v)
-                                    if (col + v < klen) w[r][v >> 1] |= static_cast<uint32_t>(__ldg(row + col + v)) << (16 * (v & 1));
-                            }
-                        }
-                    }
-#pragma unroll
-                    for (int r = 0; r < kUnroll; ++r) {
-                        if (j0 + 2 * r >= n) break;  // uniform: both halves run, the shuffles need all lanes
-                        const int j = min(j0 + 2 * r + half, NMAX - 1);
-                        const float s = g.fmt == 0 ? quant_row<0>(dst, j, l16, w[r]) : quant_row<1>(dst, j, l16, w[r]);
-                        if (l16 == 0) sc[j] = s;
+                for (int r = 0; r < (kMode == kDenseFp8 ? 0 : kUnroll); ++r) {
+                    if (j0 + kRowsAtOnce * r >= n) break;  // uniform: the shuffles need all lanes
+                    const int j = j0 + kRowsAtOnce * r + lrow;
+                    if constexpr (kQuant) {
+                        // (with an odd n the last pair's second row is one of zeros: it lies below NMAX)
+                        const uint32_t w[4] = {cur.v[r].x, cur.v[r].y, cur.v[r].z, cur.v[r].w};
+                        const float s = g.fmt == 0 ? quant_row<0>(dst, j, lane & 15, w) : quant_row<1>(dst, j, lane & 15, w);
+                        if ((lane & 15) == 0) sc[j] = s;
+                    } else if (j < n) {
+                        // 16-byte chunk c of row j sits at chunk c ^ (j % 8)
+                        *reinterpret_cast<uint4*>(dst + j * 128 + (((lane & 7) ^ (j & 7)) << 4)) = cur.v[r];
                     }
                 }
-            } else {
-                // 16-byte chunk c of row j sits at chunk c ^ (j % 8)
-                const int64_t klen = kMode == kDown ? g.inter : g.k;
-                const int c = lane & 7;
-                const int64_t col = static_cast<int64_t>(kb) * kBK + 16 * c;
-                constexpr int kUnroll = NMAX / 4 < 8 ? NMAX / 4 : 8;
-                for (int j0 = 0; j0 < n; j0 += 4 * kUnroll) {
-                    uint4 v[kUnroll];
+                cur = nxt;
 #pragma unroll
-                    for (int r = 0; r < kUnroll; ++r) {
-                        const int j = j0 + 4 * r + (lane >> 3);
-                        v[r] = make_uint4(0u, 0u, 0u, 0u);
-                        if (j < n && col < klen) {
-                            const uint8_t* row = kMode == kDown ? g.hq + static_cast<int64_t>(pairs[j]) * g.inter
-                                                                : static_cast<const uint8_t*>(g.x) + batch * g.x_batch + j * g.ldx;
-                            if (col + 16 <= klen) {  // rows are 16-byte aligned
-                                v[r] = kMode == kDown ? __ldcg(reinterpret_cast<const uint4*>(row + col))
-                                                      : __ldg(reinterpret_cast<const uint4*>(row + col));
-                            } else {
-                                uint32_t b[4] = {0u, 0u, 0u, 0u};
-#pragma unroll
-                                for (int e = 0; e < 15; ++e)
-                                    if (col + e < klen) b[e >> 2] |= static_cast<uint32_t>(row[col + e]) << (8 * (e & 3));
-                                v[r] = make_uint4(b[0], b[1], b[2], b[3]);
-                            }
-                        }
-                    }
-#pragma unroll
-                    for (int r = 0; r < kUnroll; ++r) {
-                        const int j = j0 + 4 * r + (lane >> 3);
-                        if (j < n) *reinterpret_cast<uint4*>(dst + j * 128 + ((c ^ (j & 7)) << 4)) = v[r];
-                    }
-                }
-                for (int j = lane; j < n; j += 32)
-                    sc[j] = kMode == kDown ? __ldcg(g.sh + static_cast<int64_t>(kb) * g.pairs + pairs[j])
-                                           : __ldg(g.sx.p + static_cast<int64_t>(j >> g.sx.shift) * g.sx.s_mn + kb * g.sx.s_kb +
-                                                   batch * g.sx.s_b);
+                for (int q = 0; q < kScales; ++q) sc_cur[q] = sc_nxt[q];
             }
             fence_proxy_async_smem();
             __syncwarp();
-            if (lane == 0) mbar_arrive(sfull + sslot);
+            if (lane == 0) mbar_arrive(full + st);
+            i += kBuilders;
+            c = cn;
+            n = nn;
+            st += kBuilders;
+            while (st >= R) {
+                st -= R;
+                phase ^= 1u;
+            }
         }
+        __syncwarp();
+        cluster_arrive();
+        cluster_wait();
     } else {
         // ------------------------------------------------------------------ blocks added with their scales
         const int q = warp & 3;
         const int row = q * 32 + lane;               // of the tile
-        const int grow = tile * kBM + row;           // of the weight
         float acc[kTiles][NMAX];
 #pragma unroll
         for (int t = 0; t < kTiles; ++t)
 #pragma unroll
             for (int j = 0; j < NMAX; ++j) acc[t][j] = 0.0f;
-        // scale of unit u's weight tile t for this thread's row
-        const int tiles_k = g.k_blocks;
-        auto weight_scale = [&](int u, int t) -> float {
-            const int kb = block_of(u);
-            if constexpr (kMode == kUp)
-                return ldg_pinned(g.w_scale + ((static_cast<int64_t>(entry_of(u).expert) * 2 + t) * g.row_tiles + tile) * tiles_k + kb);
-            else if constexpr (kMode == kDown)
-                return ldg_pinned(g.w_scale + (static_cast<int64_t>(entry_of(u).expert) * g.row_tiles + tile) * tiles_k + kb);
-            else
-                return grow < g.rows ? ldg_pinned(g.sw.p + static_cast<int64_t>(grow >> g.sw.shift) * g.sw.s_mn + kb * g.sw.s_kb +
-                                                  batch * g.sw.s_b)
-                                     : 0.0f;
-        };
-        float next[kTiles];
+        // weight scales of this thread's row: pointers of the current entry, a value loaded a block ahead
+        const float* sw_at[kTiles];
+        int n = g.ncols;
+        Entry en{};
+        const int64_t sw_step = kMoe ? 1 : g.sw.s_kb;
+        auto enter = [&](int ent) {
+            if constexpr (kMoe) {
+                en = entry_at(ent);
+                n = en.n;
+                const int tile = tile_of(ent);
 #pragma unroll
-        for (int t = 0; t < kTiles; ++t) next[t] = u0 < u1 ? weight_scale(u0, t) : 0.0f;
-        int buf = 0, sslot = 0;
-        uint32_t bphase = 0, sphase = 0;
+                for (int t = 0; t < kTiles; ++t)
+                    sw_at[t] = g.w_scale + ((static_cast<int64_t>(en.expert) * kTiles + t) * g.row_tiles + tile) * g.k_blocks;
+            } else {
+                const int grow = min(tile_of(0) * kBM + row, g.rows - 1);  // rows past the end are never stored
+                sw_at[0] = g.sw.p + static_cast<int64_t>(grow >> g.sw.shift) * g.sw.s_mn + batch * g.sw.s_b;
+            }
+        };
+        Cursor c = first(0);
+        float next[kTiles];
+        if (units > 0) {
+            enter(c.ent);
+#pragma unroll
+            for (int t = 0; t < kTiles; ++t) next[t] = ldg_pinned(sw_at[t] + c.kb * sw_step);
+        }
+        int st = 0;
+        uint32_t phase = 0;
         bool ok = true;
-        for (int u = u0; u < u1; ++u) {
+        for (int i = 0; i < units; ++i) {
             float sw[kTiles];
 #pragma unroll
             for (int t = 0; t < kTiles; ++t) sw[t] = next[t];
-            if (u + 1 < u1) {
+            Cursor cn = c;
+            cn.advance(1, g.k_blocks);
+            const bool last = i + 1 == units, ends = last || cn.ent != c.ent;  // ends: the entry's part is complete
+            const Entry here = en;
+            const int n_here = n;
+            if (!last) {
+                if (ends) enter(cn.ent);
 #pragma unroll
-                for (int t = 0; t < kTiles; ++t) next[t] = weight_scale(u + 1, t);
+                for (int t = 0; t < kTiles; ++t) next[t] = ldg_pinned(sw_at[t] + cn.kb * sw_step);
             }
-            const int n = kMoe ? static_cast<int>(entry_of(u).n) : g.ncols;
-            ok = mbar_wait_bounded(sfull + sslot, sphase, g.wait, abort_flag, kStatusWaitEpilogue) &&
-                 mbar_wait_bounded(acc_full + buf, bphase, g.wait, abort_flag, kStatusWaitEpilogue);
+            // (the token scales come with `full`, the sums with `done`)  A warp that gave up runs on without
+            // waiting or adding, so that the barrier at the end of an item still finds all four.
+            if (ok) ok = mbar_wait_bounded(full + st, phase, g.wait, abort_flag, kStatusWaitEpilogue) &&
+                         mbar_wait_bounded(done + st, phase, g.wait, abort_flag, kStatusWaitEpilogue);
             ok = __all_sync(0xFFFFFFFFu, ok);
-            if (!ok) break;
-            tc_fence_after_sync();
-            const float* sc = xs + sslot * NMAX;
-            const uint32_t taddr = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(buf * kBufCols);
+            if (ok) {
+                tc_fence_after_sync();
+                const float* sc = xs + st * NMAX;
+                const uint32_t taddr = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(st * kTiles * NMAX);
 #pragma unroll
-            for (int c = 0; c < NMAX; c += 16) {
-                if (c < n) {
-                    uint32_t d[kTiles][16];
+                for (int cc = 0; cc < NMAX; cc += 16) {
+                    if (cc < n_here) {
+                        uint32_t d[kTiles][16];
 #pragma unroll
-                    for (int t = 0; t < kTiles; ++t) tmem_load_16cols(taddr + t * NMAX + c, d[t]);
-                    tmem_wait_ld();
+                        for (int t = 0; t < kTiles; ++t) tmem_load_16cols(taddr + t * NMAX + cc, d[t]);
+                        tmem_wait_ld();
 #pragma unroll
-                    for (int e = 0; e < 16; e += 4) {
-                        const float4 f = *reinterpret_cast<const float4*>(sc + c + e);  // columns from n on: never stored
+                        for (int e = 0; e < 16; e += 4) {
+                            const float4 f = *reinterpret_cast<const float4*>(sc + cc + e);  // columns from n on: never stored
 #pragma unroll
-                        for (int t = 0; t < kTiles; ++t) {
-                            acc[t][c + e] = fmaf(__uint_as_float(d[t][e]), __fmul_rn(sw[t], f.x), acc[t][c + e]);
-                            acc[t][c + e + 1] = fmaf(__uint_as_float(d[t][e + 1]), __fmul_rn(sw[t], f.y), acc[t][c + e + 1]);
-                            acc[t][c + e + 2] = fmaf(__uint_as_float(d[t][e + 2]), __fmul_rn(sw[t], f.z), acc[t][c + e + 2]);
-                            acc[t][c + e + 3] = fmaf(__uint_as_float(d[t][e + 3]), __fmul_rn(sw[t], f.w), acc[t][c + e + 3]);
+                            for (int t = 0; t < kTiles; ++t) {
+                                acc[t][cc + e] = fmaf(__uint_as_float(d[t][e]), __fmul_rn(sw[t], f.x), acc[t][cc + e]);
+                                acc[t][cc + e + 1] = fmaf(__uint_as_float(d[t][e + 1]), __fmul_rn(sw[t], f.y), acc[t][cc + e + 1]);
+                                acc[t][cc + e + 2] = fmaf(__uint_as_float(d[t][e + 2]), __fmul_rn(sw[t], f.z), acc[t][cc + e + 2]);
+                                acc[t][cc + e + 3] = fmaf(__uint_as_float(d[t][e + 3]), __fmul_rn(sw[t], f.w), acc[t][cc + e + 3]);
+                            }
                         }
                     }
                 }
-            }
-            // the buffer and the scales are read
-            tc_fence_before_sync();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(acc_empty + buf);
-            if (++buf == kBufs) {
-                buf = 0;
-                bphase ^= 1u;
-            }
-            if (++sslot == kScaleSlots) {
-                sslot = 0;
-                sphase ^= 1u;
+                // the stage's sums and scales are read
+                tc_fence_before_sync();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(added + st);
+                if (++st == R) {
+                    st = 0;
+                    phase ^= 1u;
+                }
             }
             if constexpr (kMode == kDown) {
-                // the entry (or this CTA's part of it) is done: add it to its tokens' rows, which only
-                // this thread touches
-                if (u + 1 == u1 || block_of(u) + 1 == g.k_blocks) {
-                    const Entry en = entry_of(u);
+                // add the entry (or this CTA's part of it) to its tokens' rows, which only this thread touches
+                if (ends) {
 #pragma unroll
                     for (int j = 0; j < NMAX; ++j) {
-                        if (j < en.n) {
-                            const int p = table.sorted[en.start + j];
-                            float* dst = outacc + (p / g.topk) * kBM + row;
-                            *dst = fmaf(__ldg(g.weights + p), acc[0][j], *dst);
+                        if (j < here.n) {
+                            float* dst = outacc + table.token[here.start + j] * kBM + row;
+                            *dst = fmaf(table.weight[here.start + j], acc[0][j], *dst);
                         }
                         acc[0][j] = 0.0f;
                     }
                 }
             }
-        }
-        if constexpr (kMode != kDown) {
-            // [tile][column][row] over the rings: this CTA's MMAs and copies are all done
-            float* red = reinterpret_cast<float*>(smem);
-            const int n = kMoe ? (idle ? 0 : static_cast<int>(entry_of(u0).n)) : g.ncols;
-            if (ok) {
+            if constexpr (kMode == kUp) {
+                // Without a cluster the item is complete here: a thread has its row's gate and up sums, the
+                // block's maximum goes over the four warps.
+                if (ends && g.splits == 1) {
+                    float* most = reinterpret_cast<float*>(smem + g.off_out) + (c.ent & 1) * 4 * NMAX;  // [warp][column]
+                    const int tile = tile_of(c.ent), at = tile * kBM + row;
 #pragma unroll
-                for (int t = 0; t < kTiles; ++t)
+                    for (int j = 0; j < NMAX; ++j) {
+                        if (j < here.n) {
+                            acc[0][j] = at < g.inter ? gated(acc[0][j], acc[1][j]) : 0.0f;
+                            const float am = warp_max(fabsf(acc[0][j]));
+                            if (lane == 0) most[q * NMAX + j] = am;
+                        }
+                    }
+                    named_barrier(1, kEpiThreads);
 #pragma unroll
-                    for (int j = 0; j < NMAX; ++j)
-                        if (j < n) red[(t * NMAX + j) * kBM + row] = acc[t][j];
+                    for (int j = 0; j < NMAX; ++j) {
+                        if (j < here.n) {
+                            const float am = fmaxf(fmaxf(most[j], most[NMAX + j]), fmaxf(most[2 * NMAX + j], most[3 * NMAX + j]));
+                            const float s = block_step(am, g.fmt);
+                            const float v = __fmul_rn(acc[0][j], __frcp_rn(s));
+                            const int p = table.sorted[here.start + j];
+                            const uint32_t byte = g.fmt == 0 ? cvt_fp8x2<0>(v, 0.0f) : cvt_fp8x2<1>(v, 0.0f);
+                            if (at < g.inter) g.hq[static_cast<int64_t>(p) * g.inter + at] = static_cast<uint8_t>(byte);
+                            if (row == 0) g.sh[static_cast<int64_t>(tile) * g.pairs + p] = s;
+                        }
+                        acc[0][j] = acc[1][j] = 0.0f;
+                    }
+                }
             }
+            c = cn;
+        }
+        // Once every CTA of the cluster is through with its ring, the sums go (over the rings) to the CTAs that
+        // write them out: rows to row / (128 / splits), or a pair's h (which needs its whole block) to
+        // column % splits.
+        __syncwarp();
+        cluster_arrive();
+        cluster_wait();
+        if (ok && units > 0 && !(kMode == kUp && g.splits == 1)) {
+            const uint32_t recv = smem_addr(smem);
+            if constexpr (kMode == kUp) {  // [range][tile][own column][row]
+                const int per = NMAX / g.splits;
+#pragma unroll
+                for (int j = 0; j < NMAX; ++j) {
+                    if (j < n) {
+                        const int own = j % g.splits, at = (rank * kTiles * per + j / g.splits) * kBM + row;
+#pragma unroll
+                        for (int t = 0; t < kTiles; ++t)
+                            st_cluster_f32(mapa_shared(recv + static_cast<uint32_t>(at + t * per * kBM) * 4, own), acc[t][j]);
+                    }
+                }
+            } else if constexpr (kMode != kDown) {  // [range][column][own row]
+                const int per = kBM / g.splits, own = row / per;
+                const uint32_t at = mapa_shared(recv + static_cast<uint32_t>(rank * g.ncols * per + row % per) * 4, own);
+#pragma unroll
+                for (int j = 0; j < NMAX; ++j)
+                    if (j < g.ncols) st_cluster_f32(at + static_cast<uint32_t>(j * per) * 4, acc[0][j]);
+            }
+        }
+        if constexpr (kMode == kDown) {  // (zeros, too, from a CTA that had no unit)
+            const int per = kBM / g.splits, own = row / per;
+            const uint32_t at = mapa_shared(smem_addr(smem) +
+                                            static_cast<uint32_t>(rank * g.tokens * per + row % per) * 4, own);
+            for (int j = 0; j < g.tokens; ++j) st_cluster_f32(at + static_cast<uint32_t>(j * per) * 4, outacc[j * kBM + row]);
         }
     }
 
     // ---------------------------------------------------------------------- sums over the cluster
     __syncwarp();
-    cluster_sync();
+    cluster_arrive();
+    cluster_wait();  // every range's sums are here; nothing of this CTA's is read or written by a peer after it
+    const float* recv = reinterpret_cast<const float*>(smem);
     if constexpr (kMode == kUp) {
-        if (!idle) {
-            // one warp per pair, all of its 128 values: h, its block scale and bytes
-            const Entry en = table.entries[batch];
-            for (int j = rank + g.splits * warp; j < en.n; j += g.splits * (kThreads / 32)) {
-                float v[2][4] = {};
-                for (int s = 0; s < g.splits; ++s) {
-#pragma unroll
-                    for (int t = 0; t < 2; ++t) {
-                        const float4 a = ld_cluster_f4(mapa_shared(
-                            smem_addr(smem) + static_cast<uint32_t>(((t * NMAX + j) * kBM + 4 * lane) * 4), static_cast<uint32_t>(s)));
-                        v[t][0] += a.x;
-                        v[t][1] += a.y;
-                        v[t][2] += a.z;
-                        v[t][3] += a.w;
-                    }
-                }
-                const int i = tile * kBM + 4 * lane;  // inter is a multiple of 16: four rows are in or out
-                float h[4], am = 0.0f;
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    h[e] = i < g.inter ? __fdiv_rn(v[0][e], 1.0f + expf(-v[0][e])) * v[1][e] : 0.0f;
-                    am = fmaxf(am, fabsf(h[e]));
-                }
-                am = warp_max(am);
-                const float s = fmaxf(__fdiv_rn(am, g.fmt == 0 ? 448.0f : 57344.0f), 1e-12f);
-                const float inv = __frcp_rn(s);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) h[e] = __fmul_rn(h[e], inv);
-                const uint32_t bytes = g.fmt == 0 ? cvt_fp8x4<0>(h[0], h[1], h[2], h[3]) : cvt_fp8x4<1>(h[0], h[1], h[2], h[3]);
-                const int p = table.sorted[en.start + j];
-                if (i < g.inter) *reinterpret_cast<uint32_t*>(g.hq + static_cast<int64_t>(p) * g.inter + i) = bytes;
-                if (lane == 0) g.sh[static_cast<int64_t>(tile) * g.pairs + p] = s;
-            }
+        if (items > 0 && g.splits > 1) {
+            const Entry en = entry_at(0);
+            const int per = NMAX / g.splits;
+            for (int jj = warp; jj * g.splits + rank < en.n; jj += kThreads / 32)
+                form_h(g, recv, g.splits, kTiles * per * kBM, per * kBM, jj, table.sorted[en.start + jj * g.splits + rank],
+                       tile_of(0), lane);
         }
     } else {
-        // rows r0 .. r1 - 1 of the tile for every column (product) or token (experts)
-        const int r0 = (rank * kBM) / g.splits, r1 = ((rank + 1) * kBM) / g.splits;
+        // this CTA's rows of the tile for every column (product) or token (experts), four rows per item
+        const int per = kBM / g.splits, quads = per / 4;  // splits is 1, 2, 4 or 8
         const int cols = kMode == kDown ? g.tokens : g.ncols;
         const int rows = kMode == kDown ? g.hidden : g.rows;
-        const uint32_t src = smem_addr(smem) + (kMode == kDown ? static_cast<uint32_t>(g.off_out) : 0u);
-        for (int i = threadIdx.x; i < cols * (r1 - r0); i += kThreads) {
-            const int j = i / (r1 - r0), r = r0 + i % (r1 - r0);
-            const int row = tile * kBM + r;
+        for (int i = threadIdx.x; i < cols * quads; i += kThreads) {
+            const int j = i / quads, r = 4 * (i % quads);
+            const int row = tile_of(0) * kBM + rank * per + r;
             if (row >= rows) continue;
-            float v = 0.0f;
-            for (int s = 0; s < g.splits; ++s)
-                v += ld_cluster_f32(mapa_shared(src + static_cast<uint32_t>((j * kBM + r) * 4), static_cast<uint32_t>(s)));
-            if (kMode != kDown && g.bias != nullptr) v += bf16_bits_to_float(__ldg(g.bias + row));
-            g.out[batch * g.stride_o + static_cast<int64_t>(j) * g.ldo + row] = __bfloat16_as_ushort(__float2bfloat16_rn(v));
+            float v[4] = {};
+            for (int s = 0; s < g.splits; ++s) {
+                const float4 a = *reinterpret_cast<const float4*>(recv + (s * cols + j) * per + r);
+                v[0] += a.x;
+                v[1] += a.y;
+                v[2] += a.z;
+                v[3] += a.w;
+            }
+            uint16_t* dst = g.out + batch * g.stride_o + static_cast<int64_t>(j) * g.ldo + row;
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (kMode != kDown && g.bias != nullptr && row + e < rows) v[e] += bf16_bits_to_float(__ldg(g.bias + row + e));
+            if (g.out_vec && row + 4 <= rows) {
+                *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+            } else {
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (row + e < rows) dst[e] = __bfloat16_as_ushort(__float2bfloat16_rn(v[e]));
+            }
         }
     }
-    cluster_sync();  // nobody's shared memory goes away while it is read
 
     tc_fence_before_sync();
     __syncthreads();
     tc_fence_after_sync();
-    if (warp == 1) tmem_dealloc(tmem_base, kTmemCols);
+    if (warp == 1) tmem_dealloc(tmem_base, kCols);
 }
 
 template <int kMode, int NMAX>
@@ -671,31 +839,36 @@ cudaError_t kernel_setup() {
     const int dev = current_device();
     std::call_once(once[dev], [dev] {
         errs[dev] = cudaFuncSetAttribute(block_stream_kernel<kMode, NMAX>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         smem_budget(ctas_per_sm(kMode, NMAX)));
+                                         smem_budget(NMAX));
     });
     return errs[dev];
 }
 
-// Shared memory: token tiles, weight ring, scales, barriers, then `extra` bytes (the tables and, for the
-// second expert launch, the outputs); as many weight slots as the budget holds.
+// Shared memory: the ring, scales, barriers, then the table and `out_size` bytes (the second expert launch's
+// outputs, the first one's block maxima); as many stages as the budget and TMEM hold.
 template <int kMode, int NMAX>
-int launch_stream(const CUtensorMap& map, StreamArgs& g, int extra_table, int extra_out, int64_t grid, cudaStream_t stream) {
+int stages_for(int table_size, int out_size) {
+    const int fixed = kMaxStages * NMAX * 4 + kBarBytes + static_cast<int>(align_up(static_cast<size_t>(table_size), 16)) + out_size;
+    const int n = std::min(max_stages(kMode, NMAX), (smem_budget(NMAX) - fixed) / stage_bytes(kMode, NMAX));
+    return n >= min_stages(NMAX) ? n : 0;
+}
+
+template <int kMode, int NMAX>
+int launch_stream(const CUtensorMap& map_w, const CUtensorMap& map_x, StreamArgs& g, int table_size, int out_size, int64_t grid,
+                  cudaStream_t stream) {
+    // the sums' exchange lies over the ring
+    static_assert(min_stages(NMAX) * stage_bytes(kMode, NMAX) >= tiles_of(kMode) * NMAX * kBM * 4, "exchange");
+    static_assert(kMode != kDown || min_stages(NMAX) * stage_bytes(kMode, NMAX) >= (NMAX == 16 ? 16 : FP8DSA_MOE_MAX_TOKENS) * kBM * 4, "exchange");
     const cudaError_t se = kernel_setup<kMode, NMAX>();
     if (se != cudaSuccess) return fail(FP8DSA_ERR_CUDA, std::string("cudaFuncSetAttribute: ") + cudaGetErrorString(se));
-    constexpr int kTiles = kMode == kUp ? 2 : 1;
-    const int fixed = kXSlots * NMAX * kBK + kScaleSlots * NMAX * 4 + kBarBytes;
-    const int extra = static_cast<int>(align_up(static_cast<size_t>(extra_table), 16)) + extra_out;
-    const int slots = std::min(kMaxWSlots, (smem_budget(ctas_per_sm(kMode, NMAX)) - fixed - extra) / kSlotBytes);
-    // the sums' exchange lies over the token tiles and the weight ring
-    if (slots < kTiles || (kMode != kDown && kTiles * NMAX * kBM * 4 > kXSlots * NMAX * kBK + slots * kSlotBytes))
-        return fail(FP8DSA_ERR_UNSUPPORTED, "shared memory: too many tokens, experts or slots");
-    g.w_slots = slots;
-    g.off_table = fixed + slots * kSlotBytes;
-    g.off_out = g.off_table + static_cast<int>(align_up(static_cast<size_t>(extra_table), 16));
+    g.stages = stages_for<kMode, NMAX>(table_size, out_size);
+    if (g.stages == 0) return fail(FP8DSA_ERR_UNSUPPORTED, "shared memory: too many tokens, experts or slots");
+    g.off_table = g.stages * stage_bytes(kMode, NMAX) + kMaxStages * NMAX * 4 + kBarBytes;
+    g.off_out = g.off_table + static_cast<int>(align_up(static_cast<size_t>(table_size), 16));
     const int rc = wait_ctl(&g.wait);
     if (rc) return rc;
-    const cudaError_t e = launch_ex(block_stream_kernel<kMode, NMAX>, dim3(static_cast<unsigned>(grid)), dim3(kThreads),
-                                    static_cast<size_t>(g.off_out + extra_out), stream, g.splits, map, g);
+    const cudaError_t e = launch_ex(block_stream_kernel<kMode, NMAX>, dim3(static_cast<unsigned>(grid)), dim3(threads_of(NMAX)),
+                                    static_cast<size_t>(g.off_out + out_size), stream, g.splits, map_w, map_x, g);
     if (e != cudaSuccess) return fail(FP8DSA_ERR_CUDA, std::string("block stream launch: ") + cudaGetErrorString(e));
     return FP8DSA_OK;
 }
@@ -723,10 +896,18 @@ int block_stream_gemm(const BlockGemmDesc& d, bool x_is_bf16, cudaStream_t strea
     int rc = encode_tensor_map(&map, CU_TENSOR_MAP_DATA_TYPE_UINT8, d.b, d.b_mn ? d.n : d.k, outer, b_bat ? d.batch : 1,
                                d.ldb, b_bat ? d.stride_b : d.ldb * outer, 128, 128, CU_TENSOR_MAP_SWIZZLE_128B);
     if (rc) return rc;
+    CUtensorMap map_x = map;
+    const bool a_bat = d.stride_a != 0 && d.batch > 1;
+    if (!x_is_bf16) {
+        rc = encode_tensor_map(&map_x, CU_TENSOR_MAP_DATA_TYPE_UINT8, d.a, d.k, d.m, a_bat ? d.batch : 1, d.lda,
+                               a_bat ? d.stride_a : d.lda * d.m, 128, d.m <= 16 ? 16 : 64, CU_TENSOR_MAP_SWIZZLE_128B);
+        if (rc) return rc;
+    }
     StreamArgs g{};
+    g.x_batched = a_bat;
     g.k_blocks = static_cast<int>((d.k + kBK - 1) / kBK);
     g.row_tiles = static_cast<int>(row_tiles);
-    g.splits = split_for(tiles, g.k_blocks, ctas_per_sm(kDenseFp8, d.m <= 16 ? 16 : 64));
+    g.splits = split_for(tiles, g.k_blocks, ctas_per_sm(d.m <= 16 ? 16 : 64));
     g.idesc = (1u << 4) | (static_cast<uint32_t>(d.fmt_b) << 7) | (static_cast<uint32_t>(d.fmt_a) << 10) |
               (static_cast<uint32_t>(d.b_mn) << 15) | (static_cast<uint32_t>(kBM >> 4) << 24);
     g.fmt = d.fmt_a;
@@ -745,14 +926,15 @@ int block_stream_gemm(const BlockGemmDesc& d, bool x_is_bf16, cudaStream_t strea
     g.out = static_cast<uint16_t*>(d.out);
     g.ldo = d.ldo;
     g.stride_o = d.stride_o;
+    g.out_vec = (reinterpret_cast<uintptr_t>(d.out) & 7) == 0 && d.ldo % 4 == 0 && (d.batch == 1 || d.stride_o % 4 == 0);
     const int64_t grid = tiles * g.splits;
     launch_begin(kKindGemm, stream);
-    if (d.m <= 16)
-        rc = x_is_bf16 ? launch_stream<kDenseBf16, 16>(map, g, 0, 0, grid, stream)
-                       : launch_stream<kDenseFp8, 16>(map, g, 0, 0, grid, stream);
+    if (x_is_bf16)
+        rc = launch_stream<kDenseBf16, 16>(map, map, g, 0, 0, grid, stream);
+    else if (d.m <= 16)
+        rc = launch_stream<kDenseFp8, 16>(map, map_x, g, 0, 0, grid, stream);
     else
-        rc = x_is_bf16 ? launch_stream<kDenseBf16, 64>(map, g, 0, 0, grid, stream)
-                       : launch_stream<kDenseFp8, 64>(map, g, 0, 0, grid, stream);
+        rc = launch_stream<kDenseFp8, 64>(map, map_x, g, 0, 0, grid, stream);
     if (rc) return rc;
     launch_end(kKindGemmSingle, stream, 2.0 * static_cast<double>(d.m) * d.n * d.k * d.batch);
     return check_launch("block stream kernel");
@@ -779,6 +961,15 @@ bool moe_sizes_ok(int64_t tokens, int64_t topk, int64_t experts, int64_t hidden,
            hidden >= 16 && inter >= 16 && hidden % 16 == 0 && inter % 16 == 0 && hidden <= (1 << 24) && inter <= (1 << 24);
 }
 
+constexpr int kMaximaBytes = 2 * 4 * 32 * 4;  // two items, four warps, up to 32 columns
+
+// Whether both launches of an instance fit in shared memory.
+template <int NMAX>
+bool moe_fits(int tokens, int pairs, int experts) {
+    const int table = table_bytes(pairs, experts, NMAX);
+    return stages_for<kUp, NMAX>(table, kMaximaBytes) > 0 && stages_for<kDown, NMAX>(table, tokens * kBM * 4) > 0;
+}
+
 template <int NMAX>
 int moe_launch(StreamArgs g, const uint8_t* w13, const float* w13_scale, const uint8_t* w2, const float* w2_scale,
                const void* x, void* out, cudaStream_t stream) {
@@ -802,9 +993,12 @@ int moe_launch(StreamArgs g, const uint8_t* w13, const float* w13_scale, const u
     a.k_blocks = hb;
     a.row_tiles = ib;
     a.w_scale = w13_scale;
-    a.splits = split_for(static_cast<int64_t>(entries) * ib, hb, ctas_per_sm(kUp, NMAX));
+    // `entries` is the most there can be; without clusters as many CTAs as run at once walk what there is
+    a.splits = split_for(static_cast<int64_t>(entries) * ib, hb, ctas_per_sm(NMAX));
+    int64_t grid = static_cast<int64_t>(entries) * ib * a.splits;
+    if (a.splits == 1) grid = std::min<int64_t>(grid, static_cast<int64_t>(ctas_per_sm(NMAX)) * sm_count());
     launch_begin(kKindGemm, stream);
-    rc = launch_stream<kUp, NMAX>(m13, a, table, 0, static_cast<int64_t>(entries) * ib * a.splits, stream);
+    rc = launch_stream<kUp, NMAX>(m13, m13, a, table, kMaximaBytes, grid, stream);
     if (rc) return rc;
     launch_end(kKindGemmSingle, stream, 2.0 * row_flops);
 
@@ -814,9 +1008,10 @@ int moe_launch(StreamArgs g, const uint8_t* w13, const float* w13_scale, const u
     b.w_scale = w2_scale;
     b.out = static_cast<uint16_t*>(out);
     b.ldo = g.hidden;
-    b.splits = split_for(hb, static_cast<int64_t>(std::min(g.pairs, g.experts)) * ib, ctas_per_sm(kDown, NMAX));
+    b.out_vec = (reinterpret_cast<uintptr_t>(out) & 7) == 0;
+    b.splits = split_for(hb, static_cast<int64_t>(std::min(g.pairs, g.experts)) * ib, ctas_per_sm(NMAX));
     launch_begin(kKindGemm, stream);
-    rc = launch_stream<kDown, NMAX>(m2, b, table, g.tokens * kBM * 4, static_cast<int64_t>(hb) * b.splits, stream);
+    rc = launch_stream<kDown, NMAX>(m2, m2, b, table, g.tokens * kBM * 4, static_cast<int64_t>(hb) * b.splits, stream);
     if (rc) return rc;
     launch_end(kKindGemmSingle, stream, row_flops);
     return check_launch("block stream kernel");
@@ -879,7 +1074,8 @@ extern "C" int moe_forward_fp8_block(const void* x, const int* ids, const float*
     g.inter = static_cast<int>(inter);
     g.hq = static_cast<uint8_t*>(workspace) + L.hq;
     g.sh = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + L.sh);
-    // at most `tokens` pairs of an expert unless a token names it twice: runs of 16 where that is enough
-    return tokens <= 16 ? moe_launch<16>(g, w13, w13_scale, w2, w2_scale, x, out, stream)
+    // at most `tokens` pairs of an expert unless a token names it twice: runs of 16 where that is enough and the
+    // tables leave room for two CTAs per SM
+    return tokens <= 16 && moe_fits<16>(g.tokens, g.pairs, g.experts) ? moe_launch<16>(g, w13, w13_scale, w2, w2_scale, x, out, stream)
                         : moe_launch<32>(g, w13, w13_scale, w2, w2_scale, x, out, stream);
 }

@@ -180,9 +180,10 @@ struct BlockGemmDesc {
     void* out;         // bf16
 };
 int block_gemm_launch(const BlockGemmDesc& d, cudaStream_t stream);
-// The same for m <= kStreamMaxRows and a K-major A (block_stream.cu): with x_is_bf16, A is bf16 (strides in
-// elements, sa unused) and quantized to fmt_a in 1 x 128 blocks on the way.
-constexpr int64_t kStreamMaxRows = 64;
+// The same for a K-major A of few rows (block_stream.cu): up to kStreamMaxRows FP8 rows, or with x_is_bf16 up to
+// kStreamMaxBf16Rows bf16 rows (strides in elements, sa unused), quantized to fmt_a in 1 x 128 blocks on
+// the way.
+constexpr int64_t kStreamMaxRows = 64, kStreamMaxBf16Rows = 16;
 int block_stream_gemm(const BlockGemmDesc& d, bool x_is_bf16, cudaStream_t stream);
 
 // One GEMM of a launch, arguments already validated.

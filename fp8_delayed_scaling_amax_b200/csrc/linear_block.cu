@@ -12,8 +12,8 @@
 // is left by the forward for the backward.  Nothing is transposed: the tensor cores read w8 and the
 // column forms as MN-major operands.
 //
-// Launches: forward 2 (x, product) + 1 when w is bf16; one in all for at most kStreamMaxRows rows of an
-// FP8 weight, where the product quantizes x itself.  Backward 1 (g) + 1 per product + 1 for grad_b.
+// Launches: forward 2 (x, product) + 1 when w is bf16; one in all for at most kStreamMaxBf16Rows rows of
+// an FP8 weight, where the product quantizes x itself.  Backward 1 (g) + 1 per product + 1 for grad_b.
 #include <cuda_runtime.h>
 
 #include <string>
@@ -141,7 +141,7 @@ extern "C" int linear_forward_fp8_block(const void* x, const void* w, int w_is_f
         sw = j.scale_row;
     }
     const fp8_block_scale_t sb{sw, 128, blocks_of(k), 1, 0};
-    if (has_x && has_y && x8c_out == nullptr && m <= kStreamMaxRows) {
+    if (has_x && has_y && x8c_out == nullptr && m <= kStreamMaxBf16Rows) {
         const BlockGemmDesc d = product(static_cast<const uint8_t*>(x), w8, fmt, fmt, 0, 0, m, n, k, {}, sb, bias, y);
         return block_stream_gemm(d, true, stream);
     }

@@ -466,7 +466,7 @@ size_t linear_forward_fp8_block_workspace_size(int64_t m, int64_t k, int64_t n);
  *   the tokens, in `fmt`; byte tensors 16-byte aligned.
  *   workspace: dev, >= linear_forward_fp8_block_workspace_size(m, k, n) bytes, 256-byte aligned, no
  *   initial contents.  k and n must be multiples of 16.
- *   An fp8 weight with at most 64 rows of x and no x8c_out (decoding) is one launch. */
+ *   An fp8 weight with at most 16 rows of x and no x8c_out (decoding) is one launch. */
 int linear_forward_fp8_block(const void* x, const void* w, int w_is_fp8, const float* w_scale, const void* bias,
                              int64_t m, int64_t k, int64_t n, fp8_fmt_t fmt, uint8_t* w8_out,
                              float* w_scale_out, uint8_t* x8c_out, float* x8c_scale_out, void* workspace,

@@ -112,7 +112,8 @@ def check(tokens, topk, experts, hidden, inter, fmt="e4m3", seed=0, ids=None, x_
 
 @pytest.mark.parametrize("tokens,topk,experts,hidden,inter", [
     (1, 1, 1, 16, 16), (1, 2, 8, 256, 384), (1, 8, 16, 1024, 512), (3, 2, 4, 144, 272), (16, 4, 8, 512, 640),
-    (17, 3, 5, 272, 144), (64, 2, 3, 384, 256), (33, 8, 40, 256, 128), (64, 6, 64, 128, 256), (5, 2, 4, 2048, 1360)])
+    (17, 3, 5, 272, 144), (64, 2, 3, 384, 256), (33, 8, 40, 256, 128), (64, 6, 64, 128, 256), (5, 2, 4, 2048, 1360),
+    (1, 4, 6, 2048, 400), (2, 3, 4, 1280, 2048), (1, 1, 2, 128, 4096)])
 def test_moe_matches_fp64(tokens, topk, experts, hidden, inter):
     check(tokens, topk, experts, hidden, inter, seed=tokens + hidden)
 
