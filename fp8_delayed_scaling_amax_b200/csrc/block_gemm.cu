@@ -14,9 +14,10 @@
 //    own (accumulate = 0 for its first MMA), handed over with one commit; the promotion of block b overlaps the MMAs of the blocks after it.  The tile's fp32 sums live in registers for the
 //    whole K loop: 128 per thread for 256-wide tiles.
 //  * 256 x 256 tiles on CTA pairs (M = 256 MMA across two SMs, each SM loads half of B), or
-//    128 x 128 tiles on single CTAs when the pair tiles would leave most SMs idle; those may also
-//    split K over a cluster of up to 8 CTAs, whose sums are added through distributed shared memory
-//    in a fixed order (no workspace, no atomics).
+//    128 x 128 tiles on single CTAs, which may split K over a cluster of up to 8 CTAs, whose sums are
+//    added through distributed shared memory in a fixed order (no workspace, no atomics).  A model
+//    of the launch's time chooses (choose_plan).  (Splitting K over pairs measured no faster than either:
+//    2048 x 1024 x 4096 20.4 us against 18.7 on 128 x 128 tiles; the exchange of 256 x 256 sums eats it.)
 //  * a thread owns one row of the tile: its sa is one register per K block.  With sb per 128 columns
 //    the product sa * sb is one more; with sb per column each promotion warp keeps its own columns'
 //    scales of the current block in shared memory and reads them back as broadcasts.
@@ -81,7 +82,7 @@ struct Cfg {
     static constexpr int kSmem = kFixed + kStages * (kAStage + kBStage);
     static constexpr uint32_t kTxBytes = (kPair ? 2u : 1u) * (kAStage + kBStage);
     static_assert(kStages >= 4, "too few pipeline stages");
-    static_assert(kPair || kBM * (BN + kRedPad) * 4 <= kStages * (kAStage + kBStage), "split-K exchange exceeds the stages");
+    static_assert(kBM * (BN + kRedPad) * 4 <= kStages * (kAStage + kBStage), "split-K exchange exceeds the stages");
     static_assert((2 * kStages + 2 * kAccBufs + 2) * 8 <= kBarBytes, "barrier area");
 };
 
@@ -118,13 +119,8 @@ __device__ __forceinline__ void decode_tile(int tile, const BlockGemmArgs& g, in
     tn = within / gm;
 }
 
-__device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
-    float4 v;
-    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-                 : "r"(addr)
-                 : "memory");
-    return v;
+__device__ __forceinline__ void st_cluster_2xb64(uint32_t addr, uint64_t a, uint64_t b) {
+    asm volatile("st.shared::cluster.v2.b64 [%0], {%1, %2};" ::"r"(addr), "l"(a), "l"(b) : "memory");
 }
 
 template <int BN, bool kPair, bool kColScale, bool kSplit>
@@ -154,9 +150,10 @@ __global__ void __launch_bounds__(Roles<kPair>::kThreads, 1)
     pdl_trigger();
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
-    const uint32_t rank = (kPair || kSplit) ? cluster_ctarank() : 0u;  // half of the pair, or K range
-    const bool leader = !kPair || rank == 0;
-    const int group = kPair ? 2 : (kSplit ? g.splits : 1);  // CTAs that share a tile
+    const uint32_t rank = kPair ? cluster_ctarank() : 0u;                     // half of the pair
+    const int range = kSplit ? static_cast<int>(cluster_ctarank()) : 0;       // K range
+    const bool leader = rank == 0;
+    const int group = kPair ? 2 : (kSplit ? g.splits : 1);                    // CTAs that share a tile
     const int unit = static_cast<int>(blockIdx.x) / group;
     const int units = static_cast<int>(gridDim.x) / group;
 
@@ -193,8 +190,8 @@ __global__ void __launch_bounds__(Roles<kPair>::kThreads, 1)
     pdl_wait();
 
     // this CTA's K blocks: all of them, or its range of the split
-    const int kb0 = kSplit ? static_cast<int>((static_cast<int64_t>(rank) * g.k_blocks) / g.splits) : 0;
-    const int kb1 = kSplit ? static_cast<int>((static_cast<int64_t>(rank + 1) * g.k_blocks) / g.splits) : g.k_blocks;
+    const int kb0 = kSplit ? static_cast<int>((static_cast<int64_t>(range) * g.k_blocks) / g.splits) : 0;
+    const int kb1 = kSplit ? static_cast<int>((static_cast<int64_t>(range + 1) * g.k_blocks) / g.splits) : g.k_blocks;
 
     if (warp < kFirstEpiWarp) {
         if constexpr (kRegSplit) regs_release<kOtherRegs>();
@@ -316,6 +313,17 @@ __global__ void __launch_bounds__(Roles<kPair>::kThreads, 1)
         uint8_t* my_stage = sOut + ew * C::kBoxes * kOutStageBytes;
         float* my_scale = reinterpret_cast<float*>(my_stage);  // per-column scales share the output boxes
         const uint32_t acc_empty_leader = kPair ? mapa_shared(smem_addr(acc_empty), 0) : 0u;
+        // a buffer is in registers: the MMAs of a later block may overwrite it
+        auto hand_back = [&](int which) {
+            tc_fence_before_sync();
+            __syncwarp();
+            if (lane == 0) {
+                if (kPair && !leader)
+                    mbar_arrive_remote(acc_empty_leader + static_cast<uint32_t>(which * sizeof(uint64_t)));
+                else
+                    mbar_arrive(acc_empty + which);
+            }
+        };
         int buf = 0, flip = 0;
         uint32_t buf_phase = 0;
         bool ok = true;
@@ -325,45 +333,52 @@ __global__ void __launch_bounds__(Roles<kPair>::kThreads, 1)
             const int row0 = tm * C::kTileM + (kPair ? static_cast<int>(rank) * kBM : 0) + q * 32;
             const int row = row0 + lane;
             const int col0 = tn * BN + cbase;
-            // scales outside the matrix are never read: their products are never stored
+#pragma unroll
+            for (int c = 0; c < C::kEpiCols / 2; ++c) acc[c] = 0u;
+            // The next K block's scales are on their way a block ahead of their use (loads that stay where they are
+            // written).  Scales outside the matrix are never read: their products are never stored.
             constexpr int kNb = kColScale ? C::kEpiCols / 32 : 1;  // kColScale: columns col0 + lane + 32 i
             const int sb_col = col0 + (kColScale ? lane : 0);
-            const bool pa_in = row < g.m;
-            uint32_t pb_in = 0;
-#pragma unroll
-            for (int i = 0; i < kNb; ++i) pb_in |= (sb_col + 32 * i < g.n ? 1u : 0u) << i;
+            const bool pa_in = row < g.m, sb_in = sb_col < g.n;
             const float* pa = g.sa.p + static_cast<int64_t>(row >> g.sa.shift) * g.sa.s_mn + b * g.sa.s_b + kb0 * g.sa.s_kb;
             const float* pb = g.sb.p + static_cast<int64_t>(sb_col >> g.sb.shift) * g.sb.s_mn + b * g.sb.s_b + kb0 * g.sb.s_kb;
-            float sa_next = 0.0f, sb_next[kNb];
-            // the next K block's scales: loads that stay where they are written, a block ahead of their use
+            float sa_next = 0.0f, sb_next = 0.0f;
             auto fetch = [&]() {
                 sa_next = pa_in ? ldg_pinned(pa) : 0.0f;
+                if constexpr (kColScale) {
+                    // straight into this warp's half of shared memory that the last block has been added from
+                    const uint32_t dst = smem_addr(my_scale + flip * C::kEpiCols + lane);
 #pragma unroll
-                for (int i = 0; i < kNb; ++i)
-                    sb_next[i] = (pb_in >> i & 1u) != 0 ? ldg_pinned(pb + i * 32 * g.sb.s_mn) : 0.0f;
+                    for (int i = 0; i < kNb; ++i) {
+                        const bool in = sb_col + 32 * i < g.n;
+                        cp_async_f32(dst + 128 * i, in ? pb + i * 32 * g.sb.s_mn : g.sb.p, in);
+                    }
+                    cp_async_commit();
+                } else {
+                    sb_next = sb_in ? ldg_pinned(pb) : 0.0f;
+                }
                 pa += g.sa.s_kb;
                 pb += g.sb.s_kb;
             };
-            if (kb0 < kb1) fetch();
             if constexpr (kColScale) {
                 if (lane == 0) bulk_wait_group_read<0>();  // the last tile's stores have read the box
                 __syncwarp();
             }
-#pragma unroll
-            for (int c = 0; c < C::kEpiCols / 2; ++c) acc[c] = 0u;
+            if (kb0 < kb1) fetch();
 
             for (int kb = kb0; kb < kb1; ++kb) {
                 const float sa = sa_next;
                 uint64_t s2 = 0;  // RN32(sa * sb), twice
-                float* cs = my_scale + flip * C::kEpiCols;
+                const uint32_t cs_addr = smem_addr(my_scale + flip * C::kEpiCols);
+                float4 f[2][2];  // kColScale: the scales of 8 columns
                 flip ^= 1;
                 if constexpr (kColScale) {
-                    // this half was last read two blocks ago, before this warp's last __syncwarp
-#pragma unroll
-                    for (int i = 0; i < kNb; ++i) cs[lane + 32 * i] = sb_next[i];
+                    cp_async_wait_all();
                     __syncwarp();
+#pragma unroll
+                    for (int v = 0; v < 2; ++v) f[0][v] = lds_f32x4(cs_addr + 16 * v);
                 } else {
-                    const float s = __fmul_rn(sa, sb_next[0]);
+                    const float s = __fmul_rn(sa, sb_next);
                     s2 = pack_f32x2(s, s);
                 }
                 if (kb + 1 < kb1) fetch();
@@ -374,49 +389,60 @@ __global__ void __launch_bounds__(Roles<kPair>::kThreads, 1)
                 if (!ok) break;
                 tc_fence_after_sync();
                 const uint32_t taddr = tmem_mine + static_cast<uint32_t>(buf * BN);
-                // two 32-column loads in flight; a chunk's registers are loaded again as soon as it is added
-                uint32_t d[2][kChunk];
-                auto add = [&](int c, const uint32_t(&dc)[kChunk]) {
-                    if constexpr (kColScale) {
+                if constexpr (kColScale) {
+                    // 16 columns at a time; the next 16 columns' sums, and the next 8 columns' scales, are loaded while
+                    // these are added
+                    constexpr int kChunks = C::kEpiCols / 16;
+                    uint32_t d[2][16];
+                    tmem_load_16cols(taddr, d[0]);
 #pragma unroll
-                        for (int e = 0; e < kChunk; e += 4) {
-                            // RN32(sa * sb), then one fma
-                            float4 f = *reinterpret_cast<const float4*>(cs + kChunk * c + e);
-                            const int i = (kChunk * c + e) / 2;
-                            mul2_rn(f.x, f.y, sa);
-                            mul2_rn(f.z, f.w, sa);
-                            fma_f32x2(acc[i], pack_b32x2(dc[e], dc[e + 1]), pack_f32x2(f.x, f.y));
-                            fma_f32x2(acc[i + 1], pack_b32x2(dc[e + 2], dc[e + 3]), pack_f32x2(f.z, f.w));
+                    for (int c = 0; c < kChunks; ++c) {
+                        tmem_wait_ld();
+                        if (c + 1 < kChunks)
+                            tmem_load_16cols(taddr + 16 * (c + 1), d[(c + 1) & 1]);
+                        else
+                            hand_back(buf);
+                        const uint32_t(&dc)[16] = d[c & 1];
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            if (c + 1 < kChunks || h == 0) {
+#pragma unroll
+                                for (int v = 0; v < 2; ++v) f[1 - h][v] = lds_f32x4(cs_addr + (16 * c + 8 * (h + 1) + 4 * v) * 4);
+                            }
+#pragma unroll
+                            for (int v = 0; v < 2; ++v) {
+                                // RN32(sa * sb), then one fma
+                                float4 m = f[h][v];
+                                mul2_rn(m.x, m.y, sa);
+                                mul2_rn(m.z, m.w, sa);
+                                const int e = 8 * h + 4 * v;
+                                fma_f32x2(acc[8 * c + e / 2], pack_b32x2(dc[e], dc[e + 1]), pack_f32x2(m.x, m.y));
+                                fma_f32x2(acc[8 * c + e / 2 + 1], pack_b32x2(dc[e + 2], dc[e + 3]), pack_f32x2(m.z, m.w));
+                            }
                         }
-                    } else {
+                    }
+                } else {
+                    // two 32-column loads in flight; a chunk's registers are loaded again as soon as it is added
+                    uint32_t d[2][kChunk];
+                    auto add = [&](int c, const uint32_t(&dc)[kChunk]) {
 #pragma unroll
                         for (int e = 0; e < kChunk; e += 2)
                             fma_f32x2(acc[(kChunk * c + e) / 2], pack_b32x2(dc[e], dc[e + 1]), s2);
-                    }
-                };
-                constexpr int kChunks = C::kEpiCols / kChunk;
-                static_assert(kChunks % 2 == 0, "chunks in pairs");
-                tmem_load_32cols(taddr, d[0]);
-                tmem_load_32cols(taddr + kChunk, d[1]);
+                    };
+                    constexpr int kChunks = C::kEpiCols / kChunk;
+                    static_assert(kChunks % 2 == 0, "chunks in pairs");
+                    tmem_load_32cols(taddr, d[0]);
+                    tmem_load_32cols(taddr + kChunk, d[1]);
 #pragma unroll
-                for (int c = 0; c < kChunks; c += 2) {
-                    tmem_wait_ld();
-                    const bool last = c + 2 == kChunks;
-                    if (last) {
-                        // the buffer is in registers: the MMAs of a later block may overwrite it
-                        tc_fence_before_sync();
-                        __syncwarp();
-                        if (lane == 0) {
-                            if (kPair && !leader)
-                                mbar_arrive_remote(acc_empty_leader + static_cast<uint32_t>(buf * sizeof(uint64_t)));
-                            else
-                                mbar_arrive(acc_empty + buf);
-                        }
+                    for (int c = 0; c < kChunks; c += 2) {
+                        tmem_wait_ld();
+                        const bool last = c + 2 == kChunks;
+                        if (last) hand_back(buf);
+                        add(c, d[0]);
+                        if (!last) tmem_load_32cols(taddr + kChunk * (c + 2), d[0]);
+                        add(c + 1, d[1]);
+                        if (!last) tmem_load_32cols(taddr + kChunk * (c + 3), d[1]);
                     }
-                    add(c, d[0]);
-                    if (!last) tmem_load_32cols(taddr + kChunk * (c + 2), d[0]);
-                    add(c + 1, d[1]);
-                    if (!last) tmem_load_32cols(taddr + kChunk * (c + 3), d[1]);
                 }
                 if (++buf == kBufs) {
                     buf = 0;
@@ -489,41 +515,42 @@ __global__ void __launch_bounds__(Roles<kPair>::kThreads, 1)
                 }
             }
         }
-        if constexpr (kSplit) {
-            // this K range's sums, [row][column] in the stages: its MMAs and copies are all done
-            // (the last block's commit covers them); rows are kRedPad floats apart from a power of two
-            if (ok) {
-                float* red = reinterpret_cast<float*>(smem);
-                ulonglong2* dst = reinterpret_cast<ulonglong2*>(red + (q * 32 + lane) * (BN + kRedPad) + cbase);
-#pragma unroll
-                for (int c = 0; c < C::kEpiCols; c += 4) dst[c / 4] = make_ulonglong2(acc[c / 2], acc[c / 2 + 1]);
-            }
-        }
         if (lane == 0) bulk_wait_group_all();
         __syncwarp();
+        if constexpr (kSplit) {
+            // Once every range's MMAs and copies are done (the last block's commit covers a CTA's own), its sums
+            // go to the range that writes their row: [range][row of its share][column] over the stages there,
+            // rows kRedPad floats further apart than a power of two.
+            cluster_sync();
+            if (ok) {
+                const int per = kBM / g.splits, r = q * 32 + lane;
+                const uint32_t dst = mapa_shared(
+                    smem_addr(smem) + static_cast<uint32_t>(((range * per + r % per) * (BN + kRedPad) + cbase) * 4),
+                    static_cast<uint32_t>(r / per));
+#pragma unroll
+                for (int c = 0; c < C::kEpiCols; c += 4) st_cluster_2xb64(dst + c * 4, acc[c / 2], acc[c / 2 + 1]);
+            }
+            __syncwarp();
+        }
     }
 
     if constexpr (kSplit) {
-        // CTA r of the cluster adds rows [r * 128 / splits, ...) of all ranges, in range order, and
-        // writes them.  Only after the second barrier may a CTA's shared memory go away.
-        cluster_sync();
+        if (warp < kFirstEpiWarp) cluster_sync();  // (the barrier above)
+        cluster_sync();  // all sums have arrived, and nobody's shared memory is written after this
         if (warp >= kFirstEpiWarp) {
             int b, tm, tn;
             decode_tile(unit, g, b, tm, tn);
             const int et = static_cast<int>(threadIdx.x) - 32 * kFirstEpiWarp;
-            const int r0 = (static_cast<int>(rank) * kBM) / g.splits, r1 = ((static_cast<int>(rank) + 1) * kBM) / g.splits;
+            const int per = kBM / g.splits;
             constexpr int kVec = BN / 8;  // eight columns per item
-            for (int i = et; i < (r1 - r0) * kVec; i += kEpiThreads) {
-                const int rr = r0 + i / kVec, cc = (i % kVec) * 8;
-                const int row = tm * kBM + rr, col = tn * BN + cc;
+            for (int i = et; i < per * kVec; i += kEpiThreads) {
+                const int rr = i / kVec, cc = (i % kVec) * 8;
+                const int row = tm * kBM + range * per + rr, col = tn * BN + cc;
                 if (row >= g.m || col >= g.n) continue;
-                float v[8];
-#pragma unroll
-                for (int e = 0; e < 8; ++e) v[e] = 0.0f;
-                const uint32_t local = smem_addr(smem) + static_cast<uint32_t>((rr * (BN + kRedPad) + cc) * 4);
-                for (int s = 0; s < g.splits; ++s) {
-                    const uint32_t src = mapa_shared(local, static_cast<uint32_t>(s));
-                    const float4 x = ld_cluster_f4(src), y = ld_cluster_f4(src + 16);
+                float v[8] = {};
+                const float* src = reinterpret_cast<const float*>(smem) + rr * (BN + kRedPad) + cc;
+                for (int s = 0; s < g.splits; ++s, src += per * (BN + kRedPad)) {  // in range order
+                    const float4 x = *reinterpret_cast<const float4*>(src), y = *reinterpret_cast<const float4*>(src + 4);
                     v[0] += x.x; v[1] += x.y; v[2] += x.z; v[3] += x.w;
                     v[4] += y.x; v[5] += y.y; v[6] += y.z; v[7] += y.w;
                 }
@@ -543,7 +570,6 @@ __global__ void __launch_bounds__(Roles<kPair>::kThreads, 1)
                 }
             }
         }
-        cluster_sync();
     }
 
     tc_fence_before_sync();
@@ -571,53 +597,87 @@ __global__ void block_fill_kernel(uint16_t* out, int64_t m, int64_t n, int64_t l
     }
 }
 
-// Shared-memory limit of an instance and, for clusters, how many fit on the device at once.
+// Shared-memory limit of an instance, and how many groups of `group` CTAs (clusters) run at once.
 template <int BN, bool kPair, bool kColScale, bool kSplit>
-cudaError_t kernel_setup(int* max_units_out) {
+cudaError_t kernel_setup(int group, int* units_out) {
     using C = Cfg<BN, kPair>;
     static std::once_flag once[kMaxDevices];
     static cudaError_t errs[kMaxDevices];
-    static int units[kMaxDevices];
+    static int units[kMaxDevices][4];  // by log2(group)
     const int dev = current_device();
     std::call_once(once[dev], [dev] {
         auto kernel = block_gemm_kernel<BN, kPair, kColScale, kSplit>;
         errs[dev] = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
-        units[dev] = sm_count();
-        if (errs[dev] != cudaSuccess || !kPair) return;
-        cudaLaunchConfig_t cfg = {};
-        cudaLaunchAttribute at[1];
-        at[0].id = cudaLaunchAttributeClusterDimension;
-        at[0].val.clusterDim.x = 2;
-        at[0].val.clusterDim.y = 1;
-        at[0].val.clusterDim.z = 1;
-        cfg.gridDim = dim3(static_cast<unsigned>(2 * (sm_count() / 2)), 1, 1);
-        cfg.blockDim = dim3(Roles<kPair>::kThreads, 1, 1);
-        cfg.dynamicSmemBytes = C::kSmem;
-        cfg.attrs = at;
-        cfg.numAttrs = 1;
-        int n = 0;
-        units[dev] = sm_count() / 2;
-        if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) == cudaSuccess && n > 0) units[dev] = n;
-        cudaGetLastError();
+        if (errs[dev] != cudaSuccess) return;
+        for (int i = 0; i < 4; ++i) {
+            units[dev][i] = sm_count() >> i;
+            if (i == 0) continue;
+            cudaLaunchConfig_t cfg = {};
+            cudaLaunchAttribute at[1];
+            at[0].id = cudaLaunchAttributeClusterDimension;
+            at[0].val.clusterDim.x = 1u << i;
+            at[0].val.clusterDim.y = 1;
+            at[0].val.clusterDim.z = 1;
+            cfg.gridDim = dim3(static_cast<unsigned>((sm_count() >> i) << i), 1, 1);
+            cfg.blockDim = dim3(Roles<kPair>::kThreads, 1, 1);
+            cfg.dynamicSmemBytes = C::kSmem;
+            cfg.attrs = at;
+            cfg.numAttrs = 1;
+            int n = 0;
+            if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) == cudaSuccess && n > 0) units[dev][i] = n;
+            cudaGetLastError();
+        }
     });
-    *max_units_out = units[dev];
+    *units_out = units[dev][group == 1 ? 0 : group == 2 ? 1 : group == 4 ? 2 : 3];
     return errs[dev];
 }
 
 template <int BN, bool kPair, bool kColScale, bool kSplit>
 int launch_cfg(const CUtensorMap (&maps)[3], const BlockGemmArgs& g, cudaStream_t stream) {
     using C = Cfg<BN, kPair>;
+    const int group = kPair ? 2 : (kSplit ? g.splits : 1);
     int units = 0;
-    cudaError_t e = kernel_setup<BN, kPair, kColScale, kSplit>(&units);
+    cudaError_t e = kernel_setup<BN, kPair, kColScale, kSplit>(group, &units);
     if (e != cudaSuccess) return fail(FP8DSA_ERR_CUDA, std::string("cudaFuncSetAttribute: ") + cudaGetErrorString(e));
     // a split launch has one cluster per tile; the others walk the tiles
-    const int group = kPair ? 2 : (kSplit ? g.splits : 1);
     const int64_t grid = static_cast<int64_t>(kSplit ? g.num_tiles : std::min(g.num_tiles, units)) * group;
     e = launch_ex(block_gemm_kernel<BN, kPair, kColScale, kSplit>, dim3(static_cast<unsigned>(grid)),
                   dim3(Roles<kPair>::kThreads),
                   C::kSmem, stream, group, maps[0], maps[1], maps[2], g);
     if (e != cudaSuccess) return fail(FP8DSA_ERR_CUDA, std::string("block gemm launch: ") + cudaGetErrorString(e));
     return FP8DSA_OK;
+}
+
+// Tile shape and K ranges of a launch: the modelled time of every choice, in us, fitted to B200 measurements of
+// these kernels.  A K block costs 0.51 us on a pair's 256 x 256 tile (0.76 with per-column scales) and 0.50
+// (0.58) on a 128 x 128 tile, whose shared memory fills at the same rate; a pair launch has 6.0 us around
+// that (cluster launch, first load, last output), a single one 1.6; the exchange of split sums 2.0 and 0.4
+// per range.  Both sides measured: 2048 x 4096 x 1024 15.8 us on pairs, 18.8 on single CTAs; 2048 x 1024 x
+// 4096 22.8 and 18.7; 128 x 1024 x 8192 27.0 us unsplit, 18.6, 13.2 and 11.8 in 2, 4 and 8 ranges.
+struct Plan {
+    bool pair;
+    int splits;
+};
+
+Plan choose_plan(const BlockGemmDesc& d, int64_t k_blocks, bool col) {
+    auto tiles_of = [&](int64_t edge) { return ((d.m + edge - 1) / edge) * ((d.n + edge - 1) / edge) * d.batch; };
+    auto walk_us = [&](int64_t tiles, int64_t units, double kb_us, double out_us) {
+        return static_cast<double>((tiles + units - 1) / units) * (static_cast<double>(k_blocks) * kb_us + out_us);
+    };
+    Plan best{true, 1};
+    double best_us = 6.0 + walk_us(tiles_of(256), sm_count() / 2, col ? 0.76 : 0.51, 0.7);
+    const double kb_us = col ? 0.58 : 0.50;
+    const int64_t tiles = tiles_of(128);
+    for (int s = 1; s <= kMaxSplit; s *= 2) {
+        if (s > 1 && (tiles * s > sm_count() || k_blocks < 2 * s)) break;
+        const double us = s == 1 ? 1.6 + walk_us(tiles, sm_count(), kb_us, 0.6)
+                                 : 1.6 + static_cast<double>((k_blocks + s - 1) / s) * kb_us + 2.0 + 0.4 * s;
+        if (us < best_us) {
+            best_us = us;
+            best = Plan{false, s};
+        }
+    }
+    return best;
 }
 
 Scales scales_of(const fp8_block_scale_t& s) {
@@ -638,17 +698,14 @@ int block_gemm_launch(const BlockGemmDesc& d, cudaStream_t stream) {
         return check_launch("block fill kernel");
     }
     if (d.m <= kStreamMaxRows && !d.a_mn) return block_stream_gemm(d, false, stream);
-    auto tiles_of = [&](int64_t tm, int64_t tn) { return ((d.m + tm - 1) / tm) * ((d.n + tn - 1) / tn) * d.batch; };
-    // Pair tiles unless they would keep at most half of the pairs busy.
-    const bool pair = 4 * tiles_of(256, 256) > sm_count();
-    const int bn = pair ? 256 : 128;
-    const int64_t tiles = pair ? tiles_of(256, 256) : tiles_of(128, 128);
-    if (tiles > (int64_t(1) << 28)) return fail(FP8DSA_ERR_UNSUPPORTED, "too many output tiles");
     const int64_t k_blocks = (d.k + kBK - 1) / kBK;
-    // Few tiles: cut K over a cluster, as far as the SMs reach and every range keeps two blocks.
-    int splits = 1;
-    if (!pair)
-        while (splits < kMaxSplit && 2 * splits * tiles <= sm_count() && k_blocks >= 4 * splits) splits *= 2;
+    const bool col = d.sb.block_mn == 1;
+    const Plan plan = choose_plan(d, k_blocks, col);
+    const bool pair = plan.pair;
+    const int splits = plan.splits;
+    const int bn = pair ? 256 : 128;
+    const int64_t tiles = ((d.m + bn - 1) / bn) * ((d.n + bn - 1) / bn) * d.batch;
+    if (tiles > (int64_t(1) << 28)) return fail(FP8DSA_ERR_UNSUPPORTED, "too many output tiles");
 
     const bool a_bat = d.stride_a != 0 && d.batch > 1;
     const bool b_bat = d.stride_b != 0 && d.batch > 1;
@@ -676,7 +733,7 @@ int block_gemm_launch(const BlockGemmDesc& d, cudaStream_t stream) {
     g.m = static_cast<int>(d.m);
     g.n = static_cast<int>(d.n);
     g.k_blocks = static_cast<int>(k_blocks);
-    g.tiles_m = static_cast<int>((d.m + (pair ? 255 : 127)) / (pair ? 256 : 128));
+    g.tiles_m = static_cast<int>((d.m + bn - 1) / bn);
     g.tiles_n = static_cast<int>((d.n + bn - 1) / bn);
     g.num_tiles = static_cast<int>(tiles);
     g.splits = splits;
@@ -698,7 +755,6 @@ int block_gemm_launch(const BlockGemmDesc& d, cudaStream_t stream) {
     rc = wait_ctl(&g.wait);
     if (rc) return rc;
 
-    const bool col = d.sb.block_mn == 1;
     launch_begin(kKindGemm, stream);
     if (pair)
         rc = col ? launch_cfg<256, true, true, false>(maps, g, stream) : launch_cfg<256, true, false, false>(maps, g, stream);
