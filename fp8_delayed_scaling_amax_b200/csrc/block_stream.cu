@@ -10,12 +10,12 @@
 //
 // Bound by reading the weight from HBM (every byte once per launch), for the smallest sizes by latency:
 //  * a ring of stages, each a 128 x 128 weight tile (gate and up: two), a token tile, its scales and a TMEM
-//    buffer: warp 0 streams the weights by TMA, warps 3-5 build the token tiles (FP8 rows are copied with
-//    their scales, bf16 rows quantized on the way: 1 x 128 blocks never leave a tile), warps 1 and 2
-//    issue the MMAs and warps 6-9 add the blocks with their scales in fp32 registers (a thread owns
-//    one weight row).  One commit per stage frees it for the producer and hands it to the adders.
-//    A single issuer with a ring and a commit each for weights, tokens and TMEM took 1200 to 1600
-//    cycles a unit (its waits 300 of them), more than a unit's bytes take from HBM.
+//    buffer: warp 0 streams the weights by TMA, warp 1 issues the MMAs, three to five warps build the
+//    token tiles (FP8 rows come by TMA, the experts' hidden rows are copied, bf16 rows quantized on the
+//    way: 1 x 128 blocks never leave a tile) and fetch the scales, four add the blocks with their scales
+//    in fp32 registers (a thread owns one weight row).  One commit per stage frees it for the producer
+//    and hands it to the adders.  Rings and commits of their own for weights, tokens and TMEM took the
+//    issuer 1200 to 1600 cycles a unit, more than a unit's bytes take from HBM.
 //  * two CTAs per SM for up to 16 tokens: 100 to 190 KB per SM are in flight;
 //  * the contraction is cut over a cluster of up to 8 CTAs; their fp32 sums meet in distributed shared
 //    memory and are added in range order, so results do not depend on timing and no workspace is needed.
@@ -42,8 +42,7 @@ constexpr int kBM = 128;       // weight rows per tile (TMEM lanes)
 constexpr int kBK = 128;       // K per block
 constexpr int kUmmaK = 32;
 constexpr int kTileBytes = kBM * kBK;
-constexpr int kIssuers = 2;
-constexpr int kFirstBuilder = 1 + kIssuers;
+constexpr int kFirstBuilder = 2;
 constexpr int kEpiThreads = 128;
 constexpr int kMaxStages = 12;
 constexpr int kBarBytes = 512;
@@ -58,10 +57,10 @@ constexpr int smem_budget(int nmax) { return ctas_per_sm(nmax) == 2 ? 112 * 1024
 constexpr int tmem_cols(int nmax) { return 512 / ctas_per_sm(nmax); }
 constexpr int builders(int nmax) { return nmax == 16 ? 3 : 5; }
 constexpr int threads_of(int nmax) { return 32 * (kFirstBuilder + builders(nmax)) + kEpiThreads; }
-// The roles that take units in turn wait for a stage's last use without having seen the uses between: with
-// at least as many stages as takers none of them can be a whole phase behind or ahead of a barrier.
+// A builder waits for a stage's last use without having seen the uses between.  Units complete in order (one
+// thread issues all MMAs, and a unit's builder arrives before it), so with at least as many stages as
+// builders none of them can be a whole phase behind or ahead of a barrier.
 constexpr int min_stages(int nmax) { return builders(nmax); }
-static_assert(kIssuers <= 3 && min_stages(16) >= kIssuers, "issuers in turn");
 constexpr int tiles_of(int mode) { return mode == kUp ? 2 : 1; }
 constexpr int stage_bytes(int mode, int nmax) { return tiles_of(mode) * kTileBytes + nmax * kBK; }
 constexpr int max_stages(int mode, int nmax) {
@@ -185,6 +184,55 @@ __device__ __forceinline__ void build_table(const Table& t, const StreamArgs& g,
             if (valid) place(from + rank % nmax, lane, w);
             if (lane == 0) *t.total = __popc(leaders);
         }
+        __syncthreads();
+        return;
+    }
+    if (g.pairs <= kThreads) {
+        // a thread per pair: its sorted position is the number of pairs of lower experts and of earlier pairs of
+        // its own, counted eight at a time from shared memory (two passes of pairs / 8 steps; sorting with one
+        // warp took 6500 cycles for 128 pairs)
+        const int p8 = (g.pairs + 7) / 8 * 8;
+        uint32_t e = 0xFFFFu;
+        if (tid < p8) {
+            if (tid < g.pairs) {
+                const int v = __ldg(g.ids + tid);
+                if (v >= 0 && v < g.experts) e = static_cast<uint32_t>(v);
+            }
+            t.id[tid] = static_cast<uint16_t>(e);
+        }
+        const float w = kWeights && tid < g.pairs ? __ldg(g.weights + tid) : 0.0f;
+        __syncthreads();
+        int pos = 0, rank = 0, count = 0;
+        if (e != 0xFFFFu) {
+            for (int q0 = 0; q0 < p8; q0 += 8) {
+                const uint4 v = *reinterpret_cast<const uint4*>(t.id + q0);
+                const uint32_t words[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    const uint32_t o = (words[k >> 1] >> (16 * (k & 1))) & 0xFFFFu;
+                    pos += o < e;
+                    count += o == e;
+                    rank += o == e && q0 + k < tid;
+                }
+            }
+            pos += rank;
+        }
+        const bool leader = e != 0xFFFFu && rank % nmax == 0;  // the first pair of an entry
+        if (tid < p8) t.rank[tid] = leader ? static_cast<uint16_t>(pos) : 0xFFFFu;
+        if (e != 0xFFFFu) place(pos, tid, w);
+        const int leaders = __syncthreads_count(leader);
+        if (leader) {
+            int ent = 0;
+            for (int q0 = 0; q0 < p8; q0 += 8) {
+                const uint4 v = *reinterpret_cast<const uint4*>(t.rank + q0);
+                const uint32_t words[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                for (int k = 0; k < 8; ++k) ent += ((words[k >> 1] >> (16 * (k & 1))) & 0xFFFFu) < static_cast<uint32_t>(pos);
+            }
+            t.entries[ent] = Entry{static_cast<uint16_t>(e), static_cast<uint16_t>(pos),
+                                   static_cast<uint16_t>(min(nmax, count - rank)), 0};
+        }
+        if (tid == 0) *t.total = leaders;
         __syncthreads();
         return;
     }
@@ -327,14 +375,17 @@ __global__ void __launch_bounds__(threads_of(NMAX), ctas_per_sm(NMAX))
     // stage st: weight tiles [128][128] each, then the token tile [NMAX][128]; behind the ring (its length
     // is the launch's) the tokens' scales and the barriers
     uint8_t* tail = smem + g.stages * kStage;
-    float* xs = reinterpret_cast<float*>(tail);                // [kMaxStages][NMAX]
-    uint64_t* full = reinterpret_cast<uint64_t*>(tail + kMaxStages * NMAX * 4);  // weights landed and tokens written
+    // The scales' ring is twice as long: a stage is built again once its MMAs are done, when those of the unit
+    // before that have been read.
+    float* xs = reinterpret_cast<float*>(tail);                // [2 kMaxStages][NMAX] the tokens' scales
+    float* ws = xs + 2 * kMaxStages * NMAX;                    // [2 kMaxStages][2] the weight tiles' scales
+    uint64_t* full = reinterpret_cast<uint64_t*>(ws + 4 * kMaxStages);  // weights landed and tokens written
     uint64_t* done = full + kMaxStages;                        // MMAs complete
     uint64_t* added = done + kMaxStages;                       // sums and scales read
     uint64_t* drain = added + kMaxStages;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-    static_assert((3 * kMaxStages + 1) * 8 + 8 <= kBarBytes, "barrier area");
+    static_assert((3 * kMaxStages + 1) * 8 + 8 + 4 * kMaxStages * 4 <= kBarBytes, "barrier area");
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rank = static_cast<int>(cluster_ctarank());
@@ -344,10 +395,10 @@ __global__ void __launch_bounds__(threads_of(NMAX), ctas_per_sm(NMAX))
     if (threadIdx.x == 0) {
         for (int i = 0; i < R; ++i) {
             mbar_init(full + i, 2);
-            mbar_init(done + i, 1);
+            mbar_init(done + i, 2);  // the MMAs' commit, and the builder (whose scales the adders read)
             mbar_init(added + i, 4);
         }
-        mbar_init(drain, kIssuers);
+        mbar_init(drain, 1);
         *abort_flag = 0;
         fence_mbar_init();
         prefetch_tensormap(&tma_w);
@@ -450,14 +501,13 @@ __global__ void __launch_bounds__(threads_of(NMAX), ctas_per_sm(NMAX))
         __syncwarp();
         cluster_arrive();
         cluster_wait();
-    } else if (warp <= kIssuers) {
-        // ------------------------------------------------------------------ MMA issuers: units in turn
-        if (lane == 0) {
-            const int h = warp - 1;
-            int st = h, ent = -1;
+    } else if (warp == 1) {
+        // ------------------------------------------------------------------ MMA issuer
+        if (elect_one()) {
+            int st = 0, ent = -1;
             uint32_t phase = 0, idesc = g.idesc;
-            Cursor c = first(h);
-            for (int i = h; i < units; i += kIssuers, c.advance(kIssuers, g.k_blocks)) {
+            Cursor c = first(0);
+            for (int i = 0; i < units; ++i, c.advance(1, g.k_blocks)) {
                 if (c.ent != ent) {
                     ent = c.ent;
                     const int n = kMoe ? static_cast<int>(entry_at(ent).n) : g.ncols;
@@ -481,13 +531,12 @@ __global__ void __launch_bounds__(threads_of(NMAX), ctas_per_sm(NMAX))
                     }
                 }
                 umma_commit(done + st);
-                st += kIssuers;
-                if (st >= R) {
-                    st -= R;
+                if (++st == R) {
+                    st = 0;
                     phase ^= 1u;
                 }
             }
-            // every MMA the issuers sent off must complete before TMEM is released
+            // every MMA this thread issued must complete before TMEM is released
             umma_commit(drain);
             mbar_wait_bounded(drain, 0, g.wait, nullptr, kStatusWaitDrain);
         }
@@ -497,8 +546,7 @@ __global__ void __launch_bounds__(threads_of(NMAX), ctas_per_sm(NMAX))
     } else if (warp < kFirstEpi) {
         // ------------------------------------------------------------------ token tiles
         // The builders take the units in turn.  Columns from n on are left as they are: a column of the
-        // product depends on its own token only.  The next batch of rows is loaded before this one is
-        // converted and before a stage is waited for.
+        // product depends on its own token only.  A unit's first rows are loaded before its stage is waited for.
         if constexpr (kMode == kDown) pdl_wait();  // hq is the first launch's
         constexpr bool kQuant = kMode == kDenseBf16 || kMode == kUp;
         // quantizing: 16 lanes per row, 8 elements each; copying: 8 lanes per row, 16 bytes each (a product's
@@ -514,9 +562,18 @@ __global__ void __launch_bounds__(threads_of(NMAX), ctas_per_sm(NMAX))
         struct Batch {
             uint4 v[kUnroll];
         } cur, nxt;
-        float sc_cur[kScales], sc_nxt[kScales];
+        float sc_cur[kScales], sw_cur = 0.0f;
         auto columns = [&](int ent) { return kMoe ? static_cast<int>(entry_at(ent).n) : g.ncols; };
-        auto load = [&](Cursor c, int n, int j0, Batch& out, float (&scale)[kScales]) {
+        auto load = [&](Cursor c, int n, int j0, Batch& out, float (&scale)[kScales], float& w_scale) {
+            if (j0 == 0 && lane < kTiles) {
+                // the weight tile's scale (128 x 128 blocks), with the tokens': it may come from HBM, and the
+                // adders, a block ahead at most, waited for it (1300 of 2300 cycles a unit)
+                if constexpr (kMoe)
+                    w_scale = __ldg(g.w_scale + ((static_cast<int64_t>(entry_at(c.ent).expert) * kTiles + lane) * g.row_tiles +
+                                                 tile_of(c.ent)) * g.k_blocks + c.kb);
+                else if (g.sw.shift != 0)
+                    w_scale = __ldg(g.sw.p + static_cast<int64_t>(tile_of(0)) * g.sw.s_mn + c.kb * g.sw.s_kb + batch * g.sw.s_b);
+            }
             const int pos = kMoe ? static_cast<int>(entry_at(c.ent).start) : 0;
             const int64_t col = static_cast<int64_t>(c.kb) * kBK + lcol;
 #pragma unroll
@@ -553,54 +610,64 @@ __global__ void __launch_bounds__(threads_of(NMAX), ctas_per_sm(NMAX))
                 }
             }
         };
-        int i = warp - kFirstBuilder, st = i % R, n = 0;
+        int i = warp - kFirstBuilder, st = i % R, slot = i % (2 * R), n = 0;
         uint32_t phase = static_cast<uint32_t>(i / R) & 1u;
         Cursor c = first(i);
         if (i < units) {
             n = columns(c.ent);
-            load(c, n, 0, cur, sc_cur);
+            load(c, n, 0, cur, sc_cur, sw_cur);
         }
         while (i < units) {
             Cursor cn = c;
             cn.advance(kBuilders, g.k_blocks);
             const bool more = i + kBuilders < units;
             const int nn = more ? (cn.ent == c.ent ? n : columns(cn.ent)) : 0;
-            bool ok = mbar_wait_bounded(added + st, phase ^ 1u, g.wait, abort_flag, kStatusWaitProducer);
+            bool ok = mbar_wait_bounded(done + st, phase ^ 1u, g.wait, abort_flag, kStatusWaitProducer);
             ok = __all_sync(0xFFFFFFFFu, ok);
             if (!ok) break;
             uint8_t* dst = smem + st * kStage + kTiles * kTileBytes;
-            float* sc = xs + st * NMAX;
+            float* sc = xs + slot * NMAX;
+            if (lane < kTiles) ws[2 * slot + lane] = sw_cur;
             for (int j0 = 0; j0 < n; j0 += kBatch) {
                 if (!kQuant && j0 == 0) {
 #pragma unroll
                     for (int q = 0; q < kScales; ++q)
                         if (lane + 32 * q < n) sc[lane + 32 * q] = sc_cur[q];
                 }
-                if (j0 + kBatch < n)
-                    load(c, n, j0 + kBatch, nxt, sc_nxt);
-                else if (more)
-                    load(cn, nn, 0, nxt, sc_nxt);
-#pragma unroll
-                for (int r = 0; r < (kMode == kDenseFp8 ? 0 : kUnroll); ++r) {
-                    if (j0 + kRowsAtOnce * r >= n) break;  // uniform: the shuffles need all lanes
-                    const int j = j0 + kRowsAtOnce * r + lrow;
-                    if constexpr (kQuant) {
-                        // (with an odd n the last pair's second row is one of zeros: it lies below NMAX)
+                if (j0 + kBatch < n) load(c, n, j0 + kBatch, nxt, sc_cur, sw_cur);
+                if constexpr (kQuant) {
+                    // one pair of rows, or all four side by side (their shuffles and divisions overlap): the rows
+                    // from n on are zeros and lie below NMAX
+                    auto convert = [&](int r) {
+                        const int j = j0 + 2 * r + lrow;
                         const uint32_t w[4] = {cur.v[r].x, cur.v[r].y, cur.v[r].z, cur.v[r].w};
                         const float s = g.fmt == 0 ? quant_row<0>(dst, j, lane & 15, w) : quant_row<1>(dst, j, lane & 15, w);
                         if ((lane & 15) == 0) sc[j] = s;
-                    } else if (j < n) {
+                    };
+                    if (j0 + 2 >= n) {
+                        convert(0);
+                    } else {
+#pragma unroll
+                        for (int r = 0; r < kUnroll; ++r) convert(r);
+                    }
+                } else if constexpr (kMode == kDown) {
+#pragma unroll
+                    for (int r = 0; r < kUnroll; ++r) {
+                        const int j = j0 + kRowsAtOnce * r + lrow;
                         // 16-byte chunk c of row j sits at chunk c ^ (j % 8)
-                        *reinterpret_cast<uint4*>(dst + j * 128 + (((lane & 7) ^ (j & 7)) << 4)) = cur.v[r];
+                        if (j < n) *reinterpret_cast<uint4*>(dst + j * 128 + (((lane & 7) ^ (j & 7)) << 4)) = cur.v[r];
                     }
                 }
                 cur = nxt;
-#pragma unroll
-                for (int q = 0; q < kScales; ++q) sc_cur[q] = sc_nxt[q];
             }
             fence_proxy_async_smem();
             __syncwarp();
-            if (lane == 0) mbar_arrive(full + st);
+            if (lane == 0) {
+                mbar_arrive(done + st);  // before `full`: the commit stays the last arrival of a phase
+                mbar_arrive(full + st);
+            }
+            // only now: the proxy fence above waits for every load the thread has under way
+            if (more) load(cn, nn, 0, cur, sc_cur, sw_cur);
             i += kBuilders;
             c = cn;
             n = nn;
@@ -609,12 +676,17 @@ __global__ void __launch_bounds__(threads_of(NMAX), ctas_per_sm(NMAX))
                 st -= R;
                 phase ^= 1u;
             }
+            slot += kBuilders;
+            if (slot >= 2 * R) slot -= 2 * R;
         }
         __syncwarp();
         cluster_arrive();
         cluster_wait();
     } else {
         // ------------------------------------------------------------------ blocks added with their scales
+        // Two units at a time where one weight tile makes a unit: a unit's barrier, TMEM load and hand-back are
+        // mostly latency (800 cycles one by one, which bounded the second expert launch).
+        constexpr int kAtOnce = kTiles == 1 ? 2 : 1;
         const int q = warp & 3;
         const int row = q * 32 + lane;               // of the tile
         float acc[kTiles][NMAX];
@@ -622,130 +694,176 @@ __global__ void __launch_bounds__(threads_of(NMAX), ctas_per_sm(NMAX))
         for (int t = 0; t < kTiles; ++t)
 #pragma unroll
             for (int j = 0; j < NMAX; ++j) acc[t][j] = 0.0f;
-        // weight scales of this thread's row: pointers of the current entry, a value loaded a block ahead
-        const float* sw_at[kTiles];
         int n = g.ncols;
         Entry en{};
-        const int64_t sw_step = kMoe ? 1 : g.sw.s_kb;
         auto enter = [&](int ent) {
             if constexpr (kMoe) {
                 en = entry_at(ent);
                 n = en.n;
-                const int tile = tile_of(ent);
-#pragma unroll
-                for (int t = 0; t < kTiles; ++t)
-                    sw_at[t] = g.w_scale + ((static_cast<int64_t>(en.expert) * kTiles + t) * g.row_tiles + tile) * g.k_blocks;
-            } else {
-                const int grow = min(tile_of(0) * kBM + row, g.rows - 1);  // rows past the end are never stored
-                sw_at[0] = g.sw.p + static_cast<int64_t>(grow >> g.sw.shift) * g.sw.s_mn + batch * g.sw.s_b;
             }
         };
+        // a product whose weight has a scale per row: this thread's, loaded a block ahead
+        const bool row_scales = !kMoe && g.sw.shift == 0;
+        const float* sw_at = nullptr;
+        float sw_row = 0.0f;
         Cursor c = first(0);
-        float next[kTiles];
         if (units > 0) {
             enter(c.ent);
-#pragma unroll
-            for (int t = 0; t < kTiles; ++t) next[t] = ldg_pinned(sw_at[t] + c.kb * sw_step);
+            if (row_scales) {
+                const int grow = min(tile_of(0) * kBM + row, g.rows - 1);  // rows past the end are never stored
+                sw_at = g.sw.p + static_cast<int64_t>(grow) * g.sw.s_mn + batch * g.sw.s_b;
+                sw_row = ldg_pinned(sw_at + c.kb * g.sw.s_kb);
+            }
         }
-        int st = 0;
+        int st = 0, slot = 0;
         uint32_t phase = 0;
         bool ok = true;
-        for (int i = 0; i < units; ++i) {
-            float sw[kTiles];
+        for (int i = 0; i < units; i += kAtOnce) {
+            // the units of this round: stage, phase, columns, scale, and whether the entry's part ends with it
+            int u_st[kAtOnce], u_slot[kAtOnce], u_n[kAtOnce];
+            float u_sw[kAtOnce];
+            Entry u_en[kAtOnce];
+            bool u_in[kAtOnce], u_ends[kAtOnce];
+            const int ent = c.ent;
 #pragma unroll
-            for (int t = 0; t < kTiles; ++t) sw[t] = next[t];
-            Cursor cn = c;
-            cn.advance(1, g.k_blocks);
-            const bool last = i + 1 == units, ends = last || cn.ent != c.ent;  // ends: the entry's part is complete
-            const Entry here = en;
-            const int n_here = n;
-            if (!last) {
-                if (ends) enter(cn.ent);
-#pragma unroll
-                for (int t = 0; t < kTiles; ++t) next[t] = ldg_pinned(sw_at[t] + cn.kb * sw_step);
+            for (int p = 0; p < kAtOnce; ++p) {
+                u_in[p] = i + p < units;
+                u_st[p] = st;
+                u_slot[p] = slot;
+                u_n[p] = n;
+                u_en[p] = en;
+                u_sw[p] = sw_row;
+                u_ends[p] = false;
+                if (u_in[p]) {
+                    Cursor cn = c;
+                    cn.advance(1, g.k_blocks);
+                    const bool last = i + p + 1 == units;
+                    u_ends[p] = last || cn.ent != c.ent;
+                    if (!last) {
+                        if (u_ends[p]) enter(cn.ent);
+                        if (row_scales) sw_row = ldg_pinned(sw_at + cn.kb * g.sw.s_kb);
+                    }
+                    c = cn;
+                    // (scales and sums come with `done`)  A warp that gave up runs on without waiting or adding, so
+                    // that the barrier at the end of an item still finds all four.
+                    if (ok) ok = mbar_wait_bounded(done + st, phase, g.wait, abort_flag, kStatusWaitEpilogue);
+                    if (++st == R) {
+                        st = 0;
+                        phase ^= 1u;
+                    }
+                    if (++slot == 2 * R) slot = 0;
+                }
             }
-            // (the token scales come with `full`, the sums with `done`)  A warp that gave up runs on without
-            // waiting or adding, so that the barrier at the end of an item still finds all four.
-            if (ok) ok = mbar_wait_bounded(full + st, phase, g.wait, abort_flag, kStatusWaitEpilogue) &&
-                         mbar_wait_bounded(done + st, phase, g.wait, abort_flag, kStatusWaitEpilogue);
             ok = __all_sync(0xFFFFFFFFu, ok);
             if (ok) {
                 tc_fence_after_sync();
-                const float* sc = xs + st * NMAX;
-                const uint32_t taddr = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(st * kTiles * NMAX);
+                const uint32_t tmem_mine = tmem_base + (static_cast<uint32_t>(q * 32) << 16);
+                float sw[kAtOnce][kTiles];
+#pragma unroll
+                for (int p = 0; p < kAtOnce; ++p)
+#pragma unroll
+                    for (int t = 0; t < kTiles; ++t) sw[p][t] = row_scales ? u_sw[p] : ws[2 * u_slot[p] + t];
 #pragma unroll
                 for (int cc = 0; cc < NMAX; cc += 16) {
-                    if (cc < n_here) {
-                        uint32_t d[kTiles][16];
+                    uint32_t d[kAtOnce][kTiles][16];
+                    bool any = false;
 #pragma unroll
-                        for (int t = 0; t < kTiles; ++t) tmem_load_16cols(taddr + t * NMAX + cc, d[t]);
-                        tmem_wait_ld();
+                    for (int p = 0; p < kAtOnce; ++p) {
+                        if (u_in[p] && cc < u_n[p]) {
+                            any = true;
 #pragma unroll
-                        for (int e = 0; e < 16; e += 4) {
-                            const float4 f = *reinterpret_cast<const float4*>(sc + cc + e);  // columns from n on: never stored
+                            for (int t = 0; t < kTiles; ++t)
+                                tmem_load_16cols(tmem_mine + static_cast<uint32_t>((u_st[p] * kTiles + t) * NMAX + cc), d[p][t]);
+                        }
+                    }
+                    if (any) tmem_wait_ld();
 #pragma unroll
-                            for (int t = 0; t < kTiles; ++t) {
-                                acc[t][cc + e] = fmaf(__uint_as_float(d[t][e]), __fmul_rn(sw[t], f.x), acc[t][cc + e]);
-                                acc[t][cc + e + 1] = fmaf(__uint_as_float(d[t][e + 1]), __fmul_rn(sw[t], f.y), acc[t][cc + e + 1]);
-                                acc[t][cc + e + 2] = fmaf(__uint_as_float(d[t][e + 2]), __fmul_rn(sw[t], f.z), acc[t][cc + e + 2]);
-                                acc[t][cc + e + 3] = fmaf(__uint_as_float(d[t][e + 3]), __fmul_rn(sw[t], f.w), acc[t][cc + e + 3]);
+                    for (int p = 0; p < kAtOnce; ++p) {
+                        if (u_in[p] && cc < u_n[p]) {
+                            const float* sc = xs + u_slot[p] * NMAX + cc;  // columns from n on: never stored
+#pragma unroll
+                            for (int e = 0; e < 16; e += 4) {
+                                const float4 f = *reinterpret_cast<const float4*>(sc + e);
+#pragma unroll
+                                for (int t = 0; t < kTiles; ++t) {
+                                    float* at = &acc[t][cc + e];
+                                    at[0] = fmaf(__uint_as_float(d[p][t][e]), __fmul_rn(sw[p][t], f.x), at[0]);
+                                    at[1] = fmaf(__uint_as_float(d[p][t][e + 1]), __fmul_rn(sw[p][t], f.y), at[1]);
+                                    at[2] = fmaf(__uint_as_float(d[p][t][e + 2]), __fmul_rn(sw[p][t], f.z), at[2]);
+                                    at[3] = fmaf(__uint_as_float(d[p][t][e + 3]), __fmul_rn(sw[p][t], f.w), at[3]);
+                                }
+                            }
+                        }
+                        if constexpr (kMode == kDown) {
+                            // add the entry (or this CTA's part of it) to its tokens' rows, which only this thread
+                            // touches
+                            if (u_ends[p]) {
+#pragma unroll
+                                for (int j = cc; j < cc + 16; ++j) {
+                                    if (j < u_n[p]) {
+                                        float* dst = outacc + table.token[u_en[p].start + j] * kBM + row;
+                                        *dst = fmaf(table.weight[u_en[p].start + j], acc[0][j], *dst);
+                                    }
+                                    acc[0][j] = 0.0f;
+                                }
                             }
                         }
                     }
                 }
-                // the stage's sums and scales are read
+                // the stages' sums and scales are read
                 tc_fence_before_sync();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(added + st);
-                if (++st == R) {
-                    st = 0;
-                    phase ^= 1u;
-                }
-            }
-            if constexpr (kMode == kDown) {
-                // add the entry (or this CTA's part of it) to its tokens' rows, which only this thread touches
-                if (ends) {
+                if (lane < kAtOnce) {
 #pragma unroll
-                    for (int j = 0; j < NMAX; ++j) {
-                        if (j < here.n) {
-                            float* dst = outacc + table.token[here.start + j] * kBM + row;
-                            *dst = fmaf(table.weight[here.start + j], acc[0][j], *dst);
-                        }
-                        acc[0][j] = 0.0f;
-                    }
+                    for (int p = 0; p < kAtOnce; ++p)
+                        if (lane == p && u_in[p]) mbar_arrive(added + u_st[p]);
                 }
             }
             if constexpr (kMode == kUp) {
                 // Without a cluster the item is complete here: a thread has its row's gate and up sums, the
                 // block's maximum goes over the four warps.
-                if (ends && g.splits == 1) {
-                    float* most = reinterpret_cast<float*>(smem + g.off_out) + (c.ent & 1) * 4 * NMAX;  // [warp][column]
-                    const int tile = tile_of(c.ent), at = tile * kBM + row;
+                if (u_ends[0] && g.splits == 1) {
+                    float* most = reinterpret_cast<float*>(smem + g.off_out) + (ent & 1) * 4 * NMAX;  // [warp][column]
+                    const int tile = tile_of(ent), at = tile * kBM + row;
+                    // Rolled loops that pick a column's registers by comparison: this code runs once per item, and
+                    // unrolled it took 25000 cycles the first time, nearly all of them instruction fetches from
+                    // a memory system that is busy with weights.
+#pragma unroll 1
+                    for (int j = 0; j < u_en[0].n; ++j) {
+                        float gate = 0.0f, up = 0.0f;
 #pragma unroll
-                    for (int j = 0; j < NMAX; ++j) {
-                        if (j < here.n) {
-                            acc[0][j] = at < g.inter ? gated(acc[0][j], acc[1][j]) : 0.0f;
-                            const float am = warp_max(fabsf(acc[0][j]));
-                            if (lane == 0) most[q * NMAX + j] = am;
+                        for (int k = 0; k < NMAX; ++k) {
+                            if (k == j) {
+                                gate = acc[0][k];
+                                up = acc[1][k];
+                            }
                         }
+                        const float h = at < g.inter ? gated(gate, up) : 0.0f;
+#pragma unroll
+                        for (int k = 0; k < NMAX; ++k)
+                            if (k == j) acc[0][k] = h;
+                        const float am = warp_max(fabsf(h));
+                        if (lane == 0) most[q * NMAX + j] = am;
                     }
                     named_barrier(1, kEpiThreads);
+#pragma unroll 1
+                    for (int j = 0; j < u_en[0].n; ++j) {
+                        float h = 0.0f;
 #pragma unroll
-                    for (int j = 0; j < NMAX; ++j) {
-                        if (j < here.n) {
-                            const float am = fmaxf(fmaxf(most[j], most[NMAX + j]), fmaxf(most[2 * NMAX + j], most[3 * NMAX + j]));
-                            const float s = block_step(am, g.fmt);
-                            const float v = __fmul_rn(acc[0][j], __frcp_rn(s));
-                            const int p = table.sorted[here.start + j];
-                            const uint32_t byte = g.fmt == 0 ? cvt_fp8x2<0>(v, 0.0f) : cvt_fp8x2<1>(v, 0.0f);
-                            if (at < g.inter) g.hq[static_cast<int64_t>(p) * g.inter + at] = static_cast<uint8_t>(byte);
-                            if (row == 0) g.sh[static_cast<int64_t>(tile) * g.pairs + p] = s;
-                        }
-                        acc[0][j] = acc[1][j] = 0.0f;
+                        for (int k = 0; k < NMAX; ++k)
+                            if (k == j) h = acc[0][k];
+                        const float am = fmaxf(fmaxf(most[j], most[NMAX + j]), fmaxf(most[2 * NMAX + j], most[3 * NMAX + j]));
+                        const float s = block_step(am, g.fmt);
+                        const float v = __fmul_rn(h, __frcp_rn(s));
+                        const int p = table.sorted[u_en[0].start + j];
+                        const uint32_t byte = g.fmt == 0 ? cvt_fp8x2<0>(v, 0.0f) : cvt_fp8x2<1>(v, 0.0f);
+                        if (at < g.inter) g.hq[static_cast<int64_t>(p) * g.inter + at] = static_cast<uint8_t>(byte);
+                        if (row == 0) g.sh[static_cast<int64_t>(tile) * g.pairs + p] = s;
                     }
+#pragma unroll
+                    for (int j = 0; j < NMAX; ++j) acc[0][j] = acc[1][j] = 0.0f;
                 }
             }
-            c = cn;
         }
         // Once every CTA of the cluster is through with its ring, the sums go (over the rings) to the CTAs that
         // write them out: rows to row / (128 / splits), or a pair's h (which needs its whole block) to
@@ -848,7 +966,7 @@ cudaError_t kernel_setup() {
 // outputs, the first one's block maxima); as many stages as the budget and TMEM hold.
 template <int kMode, int NMAX>
 int stages_for(int table_size, int out_size) {
-    const int fixed = kMaxStages * NMAX * 4 + kBarBytes + static_cast<int>(align_up(static_cast<size_t>(table_size), 16)) + out_size;
+    const int fixed = 2 * kMaxStages * NMAX * 4 + kBarBytes + static_cast<int>(align_up(static_cast<size_t>(table_size), 16)) + out_size;
     const int n = std::min(max_stages(kMode, NMAX), (smem_budget(NMAX) - fixed) / stage_bytes(kMode, NMAX));
     return n >= min_stages(NMAX) ? n : 0;
 }
@@ -863,7 +981,7 @@ int launch_stream(const CUtensorMap& map_w, const CUtensorMap& map_x, StreamArgs
     if (se != cudaSuccess) return fail(FP8DSA_ERR_CUDA, std::string("cudaFuncSetAttribute: ") + cudaGetErrorString(se));
     g.stages = stages_for<kMode, NMAX>(table_size, out_size);
     if (g.stages == 0) return fail(FP8DSA_ERR_UNSUPPORTED, "shared memory: too many tokens, experts or slots");
-    g.off_table = g.stages * stage_bytes(kMode, NMAX) + kMaxStages * NMAX * 4 + kBarBytes;
+    g.off_table = g.stages * stage_bytes(kMode, NMAX) + 2 * kMaxStages * NMAX * 4 + kBarBytes;
     g.off_out = g.off_table + static_cast<int>(align_up(static_cast<size_t>(table_size), 16));
     const int rc = wait_ctl(&g.wait);
     if (rc) return rc;

@@ -50,6 +50,17 @@ __device__ __forceinline__ void report_status(const WaitCtl& ctl, int code) {
     if (ctl.status) atomicCAS(ctl.status, 0, code);
 }
 
+// One lane of a converged warp, in a form from which the compiler knows that the branch has one thread.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xFFFFFFFF;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(p));
+    return p != 0;
+}
+
 // ---------------------------------------------------------------------------------------
 // mbarrier (shared-memory transaction barrier)
 // ---------------------------------------------------------------------------------------
