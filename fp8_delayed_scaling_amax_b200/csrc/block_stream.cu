@@ -48,7 +48,9 @@ constexpr int kMaxStages = 12;
 constexpr int kBarBytes = 512;
 constexpr int kMaxSplit = 8;
 
-enum Mode : int { kDenseFp8 = 0, kDenseBf16 = 1, kUp = 2, kDown = 3 };
+// kUp: the first expert launch on bf16 tokens, kUpFp8: on tokens quantized before, kDown: the second launch.
+enum Mode : int { kDenseFp8 = 0, kDenseBf16 = 1, kUp = 2, kDown = 3, kUpFp8 = 4 };
+constexpr bool is_up(int mode) { return mode == kUp || mode == kUpFp8; }
 
 // Two CTAs per SM (96 registers per thread, 112 KB each) for up to 16 columns; the wide instances hold 64
 // sums per thread, or the outputs of 64 tokens, and take an SM alone.
@@ -61,7 +63,7 @@ constexpr int threads_of(int nmax) { return 32 * (kFirstBuilder + builders(nmax)
 // thread issues all MMAs, and a unit's builder arrives before it), so with at least as many stages as
 // builders none of them can be a whole phase behind or ahead of a barrier.
 constexpr int min_stages(int nmax) { return builders(nmax); }
-constexpr int tiles_of(int mode) { return mode == kUp ? 2 : 1; }
+constexpr int tiles_of(int mode) { return is_up(mode) ? 2 : 1; }
 constexpr int stage_bytes(int mode, int nmax) { return tiles_of(mode) * kTileBytes + nmax * kBK; }
 constexpr int max_stages(int mode, int nmax) {
     return tmem_cols(nmax) / (tiles_of(mode) * nmax) < kMaxStages ? tmem_cols(nmax) / (tiles_of(mode) * nmax) : kMaxStages;
@@ -97,6 +99,8 @@ struct StreamArgs {
     const float* weights;
     const float* w_scale;
     int tokens, pairs, topk, experts, hidden, inter;
+    const uint8_t* xq;          // [tokens][hidden] quantized before (more than 16 tokens)
+    const float* sxq;           // [blocks of hidden][tokens]
     uint8_t* hq;                // [pairs][inter]
     float* sh;                  // [blocks of inter][pairs]
     int off_table, off_out;     // byte offsets in shared memory
@@ -293,26 +297,43 @@ __device__ __forceinline__ float block_step(float amax, int fmt) {
     return fmaxf(__fdiv_rn(amax, fmt == 0 ? 448.0f : 57344.0f), 1e-12f);
 }
 
-// One K block of a bf16 row, 16 lanes per row (lane l16 holds elements 8 l16 ..): quantized into the
-// 128-byte-swizzled row `j` of a token tile; returns the block's scale.
-template <int kFmt>
-__device__ __forceinline__ float quant_row(uint8_t* tile, int j, int l16, const uint32_t (&w)[4]) {
-    uint32_t m = max_abs_bf16x2(max_abs_bf16x2(0u, w[0]), max_abs_bf16x2(w[1], max_abs_bf16x2(w[2], w[3])));
-    float am = fmaxf(fabsf(__uint_as_float(m << 16)), fabsf(__uint_as_float(m & 0xFFFF0000u)));
+// One K block of 2 * kPairs bf16 rows, 16 lanes per row (lane l16 holds elements 8 l16 .. of rows 2 r + lane / 16,
+// r = 0 .. kPairs - 1): quantized into the 128-byte-swizzled rows j0 .. of a token tile, with the scales.  The
+// maxima's shuffles run side by side, and each lane forms one row's scale and reciprocal for all.
+template <int kFmt, int kPairs>
+__device__ __forceinline__ void quant_rows(uint8_t* tile, float* sc, int j0, int lane, const uint4* v) {
+    const int l16 = lane & 15, half = lane >> 4;
+    float am[kPairs], mine = 0.0f;
 #pragma unroll
-    for (int o = 8; o > 0; o >>= 1) am = fmaxf(am, __shfl_xor_sync(0xFFFFFFFFu, am, o));
-    const float s = block_step(am, kFmt);
-    const float inv = __frcp_rn(s);
-    float f[8];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        f[2 * i] = __uint_as_float(w[i] << 16);
-        f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-        mul2_rn(f[2 * i], f[2 * i + 1], inv);
+    for (int r = 0; r < kPairs; ++r) {
+        const uint32_t m = max_abs_bf16x2(max_abs_bf16x2(0u, v[r].x), max_abs_bf16x2(v[r].y, max_abs_bf16x2(v[r].z, v[r].w)));
+        am[r] = fmaxf(fabsf(__uint_as_float(m << 16)), fabsf(__uint_as_float(m & 0xFFFF0000u)));
     }
-    const uint2 q = make_uint2(cvt_fp8x4<kFmt>(f[0], f[1], f[2], f[3]), cvt_fp8x4<kFmt>(f[4], f[5], f[6], f[7]));
-    *reinterpret_cast<uint2*>(tile + j * 128 + (((l16 >> 1) ^ (j & 7)) << 4) + (l16 & 1) * 8) = q;
-    return s;
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1)
+#pragma unroll
+        for (int r = 0; r < kPairs; ++r) am[r] = fmaxf(am[r], __shfl_xor_sync(0xFFFFFFFFu, am[r], o));
+#pragma unroll
+    for (int r = 0; r < kPairs; ++r)
+        if (l16 == r) mine = am[r];
+    const float s = block_step(mine, kFmt);
+    const float inv_mine = __frcp_rn(s);
+    if (l16 < kPairs) sc[j0 + 2 * l16 + half] = s;
+#pragma unroll
+    for (int r = 0; r < kPairs; ++r) {
+        const float inv = __shfl_sync(0xFFFFFFFFu, inv_mine, (half << 4) | r);
+        const uint32_t w[4] = {v[r].x, v[r].y, v[r].z, v[r].w};
+        float f[8];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            f[2 * i] = __uint_as_float(w[i] << 16);
+            f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+            mul2_rn(f[2 * i], f[2 * i + 1], inv);
+        }
+        const int j = j0 + 2 * r + half;
+        *reinterpret_cast<uint2*>(tile + j * 128 + (((l16 >> 1) ^ (j & 7)) << 4) + (l16 & 1) * 8) =
+            make_uint2(cvt_fp8x4<kFmt>(f[0], f[1], f[2], f[3]), cvt_fp8x4<kFmt>(f[4], f[5], f[6], f[7]));
+    }
 }
 
 // gate / (1 + exp(-gate)) * up in fp32
@@ -367,8 +388,9 @@ __global__ void __launch_bounds__(threads_of(NMAX), ctas_per_sm(NMAX))
     block_stream_kernel(const __grid_constant__ CUtensorMap tma_w, const __grid_constant__ CUtensorMap tma_x,
                         const __grid_constant__ StreamArgs g) {
     constexpr int kBuilders = builders(NMAX), kFirstEpi = kFirstBuilder + kBuilders, kThreads = threads_of(NMAX);
-    constexpr bool kMoe = kMode == kUp || kMode == kDown;
-    constexpr int kTiles = kMode == kUp ? 2 : 1;   // weight tiles per K block (gate and up)
+    constexpr bool kIsUp = is_up(kMode);
+    constexpr bool kMoe = kIsUp || kMode == kDown;
+    constexpr int kTiles = kIsUp ? 2 : 1;   // weight tiles per K block (gate and up)
     constexpr int kStage = stage_bytes(kMode, NMAX);
     constexpr int kCols = tmem_cols(NMAX);
     extern __shared__ __align__(1024) uint8_t smem[];
@@ -381,26 +403,26 @@ __global__ void __launch_bounds__(threads_of(NMAX), ctas_per_sm(NMAX))
     float* ws = xs + 2 * kMaxStages * NMAX;                    // [2 kMaxStages][2] the weight tiles' scales
     uint64_t* full = reinterpret_cast<uint64_t*>(ws + 4 * kMaxStages);  // weights landed and tokens written
     uint64_t* done = full + kMaxStages;                        // MMAs complete
-    uint64_t* added = done + kMaxStages;                       // sums and scales read
-    uint64_t* drain = added + kMaxStages;
+    uint64_t* drain = done + kMaxStages;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-    static_assert((3 * kMaxStages + 1) * 8 + 8 + 4 * kMaxStages * 4 <= kBarBytes, "barrier area");
+    static_assert((2 * kMaxStages + 1) * 8 + 8 + 4 * kMaxStages * 4 <= kBarBytes, "barrier area");
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rank = static_cast<int>(cluster_ctarank());
     const int R = g.stages;
-    if constexpr (kMode != kUp) pdl_trigger();
+    if constexpr (!kIsUp) pdl_trigger();
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < R; ++i) {
-            mbar_init(full + i, 2);
+            mbar_init(full + i, 6);  // the weights, the tokens, and the four adders of the unit a ring ago
             mbar_init(done + i, 2);  // the MMAs' commit, and the builder (whose scales the adders read)
-            mbar_init(added + i, 4);
         }
         mbar_init(drain, 1);
         *abort_flag = 0;
         fence_mbar_init();
+        for (int i = 0; i < R; ++i)
+            for (int w = 0; w < 4; ++w) mbar_arrive(full + i);  // nothing is there to be added at first
         prefetch_tensormap(&tma_w);
     }
     if (warp == 1) {
@@ -413,7 +435,7 @@ __global__ void __launch_bounds__(threads_of(NMAX), ctas_per_sm(NMAX))
     // The second expert launch reads only ids and weights before its wait: the first one has waited for
     // whatever wrote them before it let this launch start.
     if constexpr (kMode != kDown) pdl_wait();
-    if constexpr (kMode == kUp) pdl_trigger();
+    if constexpr (kIsUp) pdl_trigger();
     Table table{};
     if constexpr (kMoe) {
         table = table_at(smem + g.off_table, g);
@@ -430,7 +452,7 @@ __global__ void __launch_bounds__(threads_of(NMAX), ctas_per_sm(NMAX))
     const int cluster_id = static_cast<int>(blockIdx.x) / g.splits;
     const int clusters = static_cast<int>(gridDim.x) / g.splits;
     int items = 1, total = g.k_blocks;
-    if constexpr (kMode == kUp) {
+    if constexpr (kIsUp) {
         const int all = *table.total * g.row_tiles;
         items = cluster_id < all ? (all - 1 - cluster_id) / clusters + 1 : 0;  // with clusters: one or none
     }
@@ -453,8 +475,8 @@ __global__ void __launch_bounds__(threads_of(NMAX), ctas_per_sm(NMAX))
     };
     // (first launch) item of cursor entry i: expert-major, so that CTAs side by side read one expert
     auto item_of = [&](int ent) { return cluster_id + ent * clusters; };
-    auto tile_of = [&](int ent) { return kMode == kUp ? item_of(ent) % g.row_tiles : cluster_id % g.row_tiles; };
-    auto entry_at = [&](int ent) { return table.entries[kMode == kUp ? item_of(ent) / g.row_tiles : ent]; };
+    auto tile_of = [&](int ent) { return kIsUp ? item_of(ent) % g.row_tiles : cluster_id % g.row_tiles; };
+    auto entry_at = [&](int ent) { return table.entries[kIsUp ? item_of(ent) / g.row_tiles : ent]; };
     const int batch = kMoe ? 0 : cluster_id / g.row_tiles;
 
     if (warp == 0) {
@@ -506,6 +528,7 @@ __global__ void __launch_bounds__(threads_of(NMAX), ctas_per_sm(NMAX))
         if (elect_one()) {
             int st = 0, ent = -1;
             uint32_t phase = 0, idesc = g.idesc;
+            bool ready = false;  // the unit's barrier, looked at before the last unit's MMAs were issued
             Cursor c = first(0);
             for (int i = 0; i < units; ++i, c.advance(1, g.k_blocks)) {
                 if (c.ent != ent) {
@@ -513,13 +536,14 @@ __global__ void __launch_bounds__(threads_of(NMAX), ctas_per_sm(NMAX))
                     const int n = kMoe ? static_cast<int>(entry_at(ent).n) : g.ncols;
                     idesc = g.idesc | (static_cast<uint32_t>((n + 15) / 16 * 2) << 17);  // N = n up to a multiple of 16
                 }
-                if (!mbar_wait_bounded(added + st, phase ^ 1u, g.wait, abort_flag, kStatusWaitMma) ||
-                    !mbar_wait_bounded(full + st, phase, g.wait, abort_flag, kStatusWaitMma))
-                    break;
+                if (!ready && !mbar_wait_bounded(full + st, phase, g.wait, abort_flag, kStatusWaitMma)) break;
                 tc_fence_after_sync();
                 const uint32_t a_base = smem_addr(smem) + static_cast<uint32_t>(st * kStage);
                 const uint32_t b_base = a_base + kTiles * kTileBytes;
                 const uint32_t d = tmem_base + static_cast<uint32_t>(st * kTiles * NMAX);
+                const int st_next = st + 1 == R ? 0 : st + 1;
+                const uint32_t phase_next = st_next == 0 ? phase ^ 1u : phase;
+                ready = i + 1 < units && mbar_test_wait(full + st_next, phase_next);
 #pragma unroll
                 for (int t = 0; t < kTiles; ++t) {
 #pragma unroll
@@ -531,10 +555,8 @@ __global__ void __launch_bounds__(threads_of(NMAX), ctas_per_sm(NMAX))
                     }
                 }
                 umma_commit(done + st);
-                if (++st == R) {
-                    st = 0;
-                    phase ^= 1u;
-                }
+                st = st_next;
+                phase = phase_next;
             }
             // every MMA this thread issued must complete before TMEM is released
             umma_commit(drain);
@@ -552,13 +574,13 @@ __global__ void __launch_bounds__(threads_of(NMAX), ctas_per_sm(NMAX))
         // quantizing: 16 lanes per row, 8 elements each; copying: 8 lanes per row, 16 bytes each (a product's
         // FP8 rows come by TMA: only their scales are copied)
         constexpr int kRowsAtOnce = kQuant ? 2 : 4;
-        constexpr int kUnroll = kMode == kDenseFp8 ? 1 : kQuant ? 4 : NMAX / 4;
+        constexpr int kUnroll = kMode == kDenseFp8 ? 1 : NMAX / 4;
         static_assert(kQuant || kMode == kDenseFp8 || NMAX <= 32, "a copied tile is one batch");
         constexpr int kBatch = kMode == kDenseFp8 ? NMAX : kRowsAtOnce * kUnroll;
         constexpr int kScales = kQuant ? 1 : (NMAX + 31) / 32;  // copying: scales per lane
         const int lrow = kQuant ? lane >> 4 : lane >> 3;        // row within kRowsAtOnce
         const int lcol = kQuant ? (lane & 15) * 8 : (lane & 7) * 16;
-        const int64_t klen = kMode == kUp ? g.hidden : kMode == kDown ? g.inter : g.k;
+        const int64_t klen = kIsUp ? g.hidden : kMode == kDown ? g.inter : g.k;
         struct Batch {
             uint4 v[kUnroll];
         } cur, nxt;
@@ -593,8 +615,10 @@ __global__ void __launch_bounds__(threads_of(NMAX), ctas_per_sm(NMAX))
                             if (col + e < klen) w[e >> 1] |= static_cast<uint32_t>(__ldg(row + col + e)) << (16 * (e & 1));
                         out.v[r] = make_uint4(w[0], w[1], w[2], w[3]);
                     }
-                } else if constexpr (kMode == kDown) {  // inter is a multiple of 16
-                    out.v[r] = __ldcg(reinterpret_cast<const uint4*>(g.hq + static_cast<int64_t>(table.sorted[pos + j]) * g.inter + col));
+                } else {  // (hidden and inter are multiples of 16)
+                    const uint8_t* row = kMode == kDown ? g.hq + static_cast<int64_t>(table.sorted[pos + j]) * g.inter
+                                                        : g.xq + static_cast<int64_t>(table.token[pos + j]) * g.hidden;
+                    out.v[r] = __ldcg(reinterpret_cast<const uint4*>(row + col));
                 }
             }
             if (!kQuant && j0 == 0) {
@@ -605,6 +629,8 @@ __global__ void __launch_bounds__(threads_of(NMAX), ctas_per_sm(NMAX))
                     if (j < n)
                         scale[q] = kMode == kDown
                                        ? __ldcg(g.sh + static_cast<int64_t>(c.kb) * g.pairs + table.sorted[pos + j])
+                                   : kMode == kUpFp8
+                                       ? __ldcg(g.sxq + static_cast<int64_t>(c.kb) * g.tokens + table.token[pos + j])
                                        : __ldg(g.sx.p + static_cast<int64_t>(j >> g.sx.shift) * g.sx.s_mn + c.kb * g.sx.s_kb +
                                                batch * g.sx.s_b);
                 }
@@ -636,21 +662,18 @@ __global__ void __launch_bounds__(threads_of(NMAX), ctas_per_sm(NMAX))
                 }
                 if (j0 + kBatch < n) load(c, n, j0 + kBatch, nxt, sc_cur, sw_cur);
                 if constexpr (kQuant) {
-                    // one pair of rows, or all four side by side (their shuffles and divisions overlap): the rows
-                    // from n on are zeros and lie below NMAX
-                    auto convert = [&](int r) {
-                        const int j = j0 + 2 * r + lrow;
-                        const uint32_t w[4] = {cur.v[r].x, cur.v[r].y, cur.v[r].z, cur.v[r].w};
-                        const float s = g.fmt == 0 ? quant_row<0>(dst, j, lane & 15, w) : quant_row<1>(dst, j, lane & 15, w);
-                        if ((lane & 15) == 0) sc[j] = s;
-                    };
+                    // one pair of rows, or the whole batch: the rows from n on are zeros and lie below NMAX
                     if (j0 + 2 >= n) {
-                        convert(0);
+                        if (g.fmt == 0)
+                            quant_rows<0, 1>(dst, sc, j0, lane, cur.v);
+                        else
+                            quant_rows<1, 1>(dst, sc, j0, lane, cur.v);
+                    } else if (g.fmt == 0) {
+                        quant_rows<0, kUnroll>(dst, sc, j0, lane, cur.v);
                     } else {
-#pragma unroll
-                        for (int r = 0; r < kUnroll; ++r) convert(r);
+                        quant_rows<1, kUnroll>(dst, sc, j0, lane, cur.v);
                     }
-                } else if constexpr (kMode == kDown) {
+                } else if constexpr (kMode != kDenseFp8) {
 #pragma unroll
                     for (int r = 0; r < kUnroll; ++r) {
                         const int j = j0 + kRowsAtOnce * r + lrow;
@@ -685,7 +708,8 @@ __global__ void __launch_bounds__(threads_of(NMAX), ctas_per_sm(NMAX))
     } else {
         // ------------------------------------------------------------------ blocks added with their scales
         // Two units at a time where one weight tile makes a unit: a unit's barrier, TMEM load and hand-back are
-        // mostly latency (800 cycles one by one, which bounded the second expert launch).
+        // mostly latency (800 cycles one by one, which bounded the second expert launch).  Loops over columns
+        // outside the K loop are rolled: little code, little of it fetched.
         constexpr int kAtOnce = kTiles == 1 ? 2 : 1;
         const int q = warp & 3;
         const int row = q * 32 + lane;               // of the tile
@@ -718,32 +742,27 @@ __global__ void __launch_bounds__(threads_of(NMAX), ctas_per_sm(NMAX))
         int st = 0, slot = 0;
         uint32_t phase = 0;
         bool ok = true;
-        for (int i = 0; i < units; i += kAtOnce) {
-            // the units of this round: stage, phase, columns, scale, and whether the entry's part ends with it
-            int u_st[kAtOnce], u_slot[kAtOnce], u_n[kAtOnce];
+        for (int i = 0; i < units;) {
+            // the units of this round: one, or two of the same entry
+            int u_st[kAtOnce], u_slot[kAtOnce], count = 0;
             float u_sw[kAtOnce];
-            Entry u_en[kAtOnce];
-            bool u_in[kAtOnce], u_ends[kAtOnce];
-            const int ent = c.ent;
+            bool ends = false;  // the entry (or this CTA's part of it) is complete with the round
+            const int ent = c.ent, n_here = n;
+            const Entry here = en;
 #pragma unroll
             for (int p = 0; p < kAtOnce; ++p) {
-                u_in[p] = i + p < units;
                 u_st[p] = st;
                 u_slot[p] = slot;
-                u_n[p] = n;
-                u_en[p] = en;
                 u_sw[p] = sw_row;
-                u_ends[p] = false;
-                if (u_in[p]) {
-                    Cursor cn = c;
-                    cn.advance(1, g.k_blocks);
-                    const bool last = i + p + 1 == units;
-                    u_ends[p] = last || cn.ent != c.ent;
-                    if (!last) {
-                        if (u_ends[p]) enter(cn.ent);
-                        if (row_scales) sw_row = ldg_pinned(sw_at + cn.kb * g.sw.s_kb);
+                if (i < units && !ends) {
+                    ++i;
+                    ++count;
+                    c.advance(1, g.k_blocks);
+                    ends = i == units || c.ent != ent;
+                    if (i < units) {
+                        if (ends) enter(c.ent);
+                        if (row_scales) sw_row = ldg_pinned(sw_at + c.kb * g.sw.s_kb);
                     }
-                    c = cn;
                     // (scales and sums come with `done`)  A warp that gave up runs on without waiting or adding, so
                     // that the barrier at the end of an item still finds all four.
                     if (ok) ok = mbar_wait_bounded(done + st, phase, g.wait, abort_flag, kStatusWaitEpilogue);
@@ -765,46 +784,28 @@ __global__ void __launch_bounds__(threads_of(NMAX), ctas_per_sm(NMAX))
                     for (int t = 0; t < kTiles; ++t) sw[p][t] = row_scales ? u_sw[p] : ws[2 * u_slot[p] + t];
 #pragma unroll
                 for (int cc = 0; cc < NMAX; cc += 16) {
-                    uint32_t d[kAtOnce][kTiles][16];
-                    bool any = false;
+                    if (cc >= n_here) break;
+                    // two units side by side, or a unit's two tiles one after the other (registers)
 #pragma unroll
-                    for (int p = 0; p < kAtOnce; ++p) {
-                        if (u_in[p] && cc < u_n[p]) {
-                            any = true;
+                    for (int t = 0; t < kTiles; ++t) {
+                        uint32_t d[kAtOnce][16];
 #pragma unroll
-                            for (int t = 0; t < kTiles; ++t)
-                                tmem_load_16cols(tmem_mine + static_cast<uint32_t>((u_st[p] * kTiles + t) * NMAX + cc), d[p][t]);
-                        }
-                    }
-                    if (any) tmem_wait_ld();
+                        for (int p = 0; p < kAtOnce; ++p)
+                            if (p < count)
+                                tmem_load_16cols(tmem_mine + static_cast<uint32_t>((u_st[p] * kTiles + t) * NMAX + cc), d[p]);
+                        tmem_wait_ld();
 #pragma unroll
-                    for (int p = 0; p < kAtOnce; ++p) {
-                        if (u_in[p] && cc < u_n[p]) {
-                            const float* sc = xs + u_slot[p] * NMAX + cc;  // columns from n on: never stored
+                        for (int p = 0; p < kAtOnce; ++p) {
+                            if (p < count) {
+                                const float* sc = xs + u_slot[p] * NMAX + cc;  // columns from n on: never stored
 #pragma unroll
-                            for (int e = 0; e < 16; e += 4) {
-                                const float4 f = *reinterpret_cast<const float4*>(sc + e);
-#pragma unroll
-                                for (int t = 0; t < kTiles; ++t) {
+                                for (int e = 0; e < 16; e += 4) {
+                                    const float4 f = *reinterpret_cast<const float4*>(sc + e);
                                     float* at = &acc[t][cc + e];
-                                    at[0] = fmaf(__uint_as_float(d[p][t][e]), __fmul_rn(sw[p][t], f.x), at[0]);
-                                    at[1] = fmaf(__uint_as_float(d[p][t][e + 1]), __fmul_rn(sw[p][t], f.y), at[1]);
-                                    at[2] = fmaf(__uint_as_float(d[p][t][e + 2]), __fmul_rn(sw[p][t], f.z), at[2]);
-                                    at[3] = fmaf(__uint_as_float(d[p][t][e + 3]), __fmul_rn(sw[p][t], f.w), at[3]);
-                                }
-                            }
-                        }
-                        if constexpr (kMode == kDown) {
-                            // add the entry (or this CTA's part of it) to its tokens' rows, which only this thread
-                            // touches
-                            if (u_ends[p]) {
-#pragma unroll
-                                for (int j = cc; j < cc + 16; ++j) {
-                                    if (j < u_n[p]) {
-                                        float* dst = outacc + table.token[u_en[p].start + j] * kBM + row;
-                                        *dst = fmaf(table.weight[u_en[p].start + j], acc[0][j], *dst);
-                                    }
-                                    acc[0][j] = 0.0f;
+                                    at[0] = fmaf(__uint_as_float(d[p][e]), __fmul_rn(sw[p][t], f.x), at[0]);
+                                    at[1] = fmaf(__uint_as_float(d[p][e + 1]), __fmul_rn(sw[p][t], f.y), at[1]);
+                                    at[2] = fmaf(__uint_as_float(d[p][e + 2]), __fmul_rn(sw[p][t], f.z), at[2]);
+                                    at[3] = fmaf(__uint_as_float(d[p][e + 3]), __fmul_rn(sw[p][t], f.w), at[3]);
                                 }
                             }
                         }
@@ -813,23 +814,39 @@ __global__ void __launch_bounds__(threads_of(NMAX), ctas_per_sm(NMAX))
                 // the stages' sums and scales are read
                 tc_fence_before_sync();
                 __syncwarp();
-                if (lane < kAtOnce) {
+                if (lane == 0) {
 #pragma unroll
                     for (int p = 0; p < kAtOnce; ++p)
-                        if (lane == p && u_in[p]) mbar_arrive(added + u_st[p]);
+                        if (p < count) mbar_arrive(full + u_st[p]);
                 }
             }
-            if constexpr (kMode == kUp) {
+            if constexpr (kMode == kDown) {
+                // add the entry to its tokens' rows, which only this thread touches
+                if (ends) {
+#pragma unroll 1
+                    for (int j = 0; j < here.n; ++j) {
+                        float v = 0.0f;
+#pragma unroll
+                        for (int k = 0; k < NMAX; ++k)
+                            if (k == j) v = acc[0][k];
+                        float* dst = outacc + table.token[here.start + j] * kBM + row;
+                        *dst = fmaf(table.weight[here.start + j], v, *dst);
+                    }
+#pragma unroll
+                    for (int k = 0; k < NMAX; ++k) acc[0][k] = 0.0f;
+                }
+            }
+            if constexpr (kIsUp) {
                 // Without a cluster the item is complete here: a thread has its row's gate and up sums, the
                 // block's maximum goes over the four warps.
-                if (u_ends[0] && g.splits == 1) {
+                if (ends && g.splits == 1) {
                     float* most = reinterpret_cast<float*>(smem + g.off_out) + (ent & 1) * 4 * NMAX;  // [warp][column]
                     const int tile = tile_of(ent), at = tile * kBM + row;
                     // Rolled loops that pick a column's registers by comparison: this code runs once per item, and
                     // unrolled it took 25000 cycles the first time, nearly all of them instruction fetches from
                     // a memory system that is busy with weights.
 #pragma unroll 1
-                    for (int j = 0; j < u_en[0].n; ++j) {
+                    for (int j = 0; j < here.n; ++j) {
                         float gate = 0.0f, up = 0.0f;
 #pragma unroll
                         for (int k = 0; k < NMAX; ++k) {
@@ -847,7 +864,7 @@ __global__ void __launch_bounds__(threads_of(NMAX), ctas_per_sm(NMAX))
                     }
                     named_barrier(1, kEpiThreads);
 #pragma unroll 1
-                    for (int j = 0; j < u_en[0].n; ++j) {
+                    for (int j = 0; j < here.n; ++j) {
                         float h = 0.0f;
 #pragma unroll
                         for (int k = 0; k < NMAX; ++k)
@@ -855,7 +872,7 @@ __global__ void __launch_bounds__(threads_of(NMAX), ctas_per_sm(NMAX))
                         const float am = fmaxf(fmaxf(most[j], most[NMAX + j]), fmaxf(most[2 * NMAX + j], most[3 * NMAX + j]));
                         const float s = block_step(am, g.fmt);
                         const float v = __fmul_rn(h, __frcp_rn(s));
-                        const int p = table.sorted[u_en[0].start + j];
+                        const int p = table.sorted[here.start + j];
                         const uint32_t byte = g.fmt == 0 ? cvt_fp8x2<0>(v, 0.0f) : cvt_fp8x2<1>(v, 0.0f);
                         if (at < g.inter) g.hq[static_cast<int64_t>(p) * g.inter + at] = static_cast<uint8_t>(byte);
                         if (row == 0) g.sh[static_cast<int64_t>(tile) * g.pairs + p] = s;
@@ -871,9 +888,9 @@ __global__ void __launch_bounds__(threads_of(NMAX), ctas_per_sm(NMAX))
         __syncwarp();
         cluster_arrive();
         cluster_wait();
-        if (ok && units > 0 && !(kMode == kUp && g.splits == 1)) {
+        if (ok && units > 0 && !(kIsUp && g.splits == 1)) {
             const uint32_t recv = smem_addr(smem);
-            if constexpr (kMode == kUp) {  // [range][tile][own column][row]
+            if constexpr (kIsUp) {  // [range][tile][own column][row]
                 const int per = NMAX / g.splits;
 #pragma unroll
                 for (int j = 0; j < NMAX; ++j) {
@@ -905,7 +922,7 @@ __global__ void __launch_bounds__(threads_of(NMAX), ctas_per_sm(NMAX))
     cluster_arrive();
     cluster_wait();  // every range's sums are here; nothing of this CTA's is read or written by a peer after it
     const float* recv = reinterpret_cast<const float*>(smem);
-    if constexpr (kMode == kUp) {
+    if constexpr (kIsUp) {
         if (items > 0 && g.splits > 1) {
             const Entry en = entry_at(0);
             const int per = NMAX / g.splits;
@@ -976,7 +993,7 @@ int launch_stream(const CUtensorMap& map_w, const CUtensorMap& map_x, StreamArgs
                   cudaStream_t stream) {
     // the sums' exchange lies over the ring
     static_assert(min_stages(NMAX) * stage_bytes(kMode, NMAX) >= tiles_of(kMode) * NMAX * kBM * 4, "exchange");
-    static_assert(kMode != kDown || min_stages(NMAX) * stage_bytes(kMode, NMAX) >= (NMAX == 16 ? 16 : FP8DSA_MOE_MAX_TOKENS) * kBM * 4, "exchange");
+    static_assert(kMode != kDown || min_stages(NMAX) * stage_bytes(kMode, NMAX) >= FP8DSA_MOE_MAX_TOKENS * kBM * 4, "exchange");
     const cudaError_t se = kernel_setup<kMode, NMAX>();
     if (se != cudaSuccess) return fail(FP8DSA_ERR_CUDA, std::string("cudaFuncSetAttribute: ") + cudaGetErrorString(se));
     g.stages = stages_for<kMode, NMAX>(table_size, out_size);
@@ -1063,14 +1080,16 @@ namespace {
 constexpr int64_t kMaxTokens = FP8DSA_MOE_MAX_TOKENS, kMaxTopk = FP8DSA_MOE_MAX_TOPK, kMaxExperts = FP8DSA_MOE_MAX_EXPERTS;
 
 struct MoeLayout {
-    size_t hq, sh, total;
+    size_t hq, sh, xq, sxq, total;
 };
-MoeLayout moe_layout(int64_t tokens, int64_t topk, int64_t inter) {
+MoeLayout moe_layout(int64_t tokens, int64_t topk, int64_t hidden, int64_t inter) {
     MoeLayout L;
     const size_t pairs = static_cast<size_t>(tokens) * topk;
     L.hq = 0;
     L.sh = align_up(pairs * static_cast<size_t>(inter), 256);
-    L.total = align_up(L.sh + pairs * static_cast<size_t>((inter + 127) / 128) * sizeof(float), 256);
+    L.xq = align_up(L.sh + pairs * static_cast<size_t>((inter + 127) / 128) * sizeof(float), 256);
+    L.sxq = align_up(L.xq + static_cast<size_t>(tokens) * hidden, 256);
+    L.total = align_up(L.sxq + static_cast<size_t>(tokens) * static_cast<size_t>((hidden + 127) / 128) * sizeof(float), 256);
     return L;
 }
 
@@ -1079,13 +1098,16 @@ bool moe_sizes_ok(int64_t tokens, int64_t topk, int64_t experts, int64_t hidden,
            hidden >= 16 && inter >= 16 && hidden % 16 == 0 && inter % 16 == 0 && hidden <= (1 << 24) && inter <= (1 << 24);
 }
 
+// More tokens than this are quantized by a launch of their own.
+constexpr int64_t kQuantizeBefore = 16;
+
 constexpr int kMaximaBytes = 2 * 4 * 32 * 4;  // two items, four warps, up to 32 columns
 
 // Whether both launches of an instance fit in shared memory.
 template <int NMAX>
 bool moe_fits(int tokens, int pairs, int experts) {
     const int table = table_bytes(pairs, experts, NMAX);
-    return stages_for<kUp, NMAX>(table, kMaximaBytes) > 0 && stages_for<kDown, NMAX>(table, tokens * kBM * 4) > 0;
+    return stages_for<kUpFp8, NMAX>(table, kMaximaBytes) > 0 && stages_for<kDown, NMAX>(table, tokens * kBM * 4) > 0;
 }
 
 template <int NMAX>
@@ -1108,6 +1130,17 @@ int moe_launch(StreamArgs g, const uint8_t* w13, const float* w13_scale, const u
     a.x = x;
     a.ldx = g.hidden;
     a.x_vec = aligned16(x);
+    if (g.xq != nullptr) {  // the tokens are quantized once, not by every CTA that reads them
+        BlockQuantJob j;
+        j.x = x;
+        j.rows = g.tokens;
+        j.cols = g.hidden;
+        j.fmt = static_cast<fp8_fmt_t>(g.fmt);
+        j.out_row = const_cast<uint8_t*>(g.xq);
+        j.scale_row = const_cast<float*>(g.sxq);
+        rc = launch_block_quantize(j, stream);
+        if (rc) return rc;
+    }
     a.k_blocks = hb;
     a.row_tiles = ib;
     a.w_scale = w13_scale;
@@ -1116,7 +1149,8 @@ int moe_launch(StreamArgs g, const uint8_t* w13, const float* w13_scale, const u
     int64_t grid = static_cast<int64_t>(entries) * ib * a.splits;
     if (a.splits == 1) grid = std::min<int64_t>(grid, static_cast<int64_t>(ctas_per_sm(NMAX)) * sm_count());
     launch_begin(kKindGemm, stream);
-    rc = launch_stream<kUp, NMAX>(m13, m13, a, table, kMaximaBytes, grid, stream);
+    rc = g.xq != nullptr ? launch_stream<kUpFp8, NMAX>(m13, m13, a, table, kMaximaBytes, grid, stream)
+                         : launch_stream<kUp, NMAX>(m13, m13, a, table, kMaximaBytes, grid, stream);
     if (rc) return rc;
     launch_end(kKindGemmSingle, stream, 2.0 * row_flops);
 
@@ -1143,7 +1177,7 @@ using namespace fp8dsa;
 extern "C" size_t moe_forward_fp8_block_workspace_size(int64_t tokens, int64_t topk, int64_t experts, int64_t hidden,
                                                        int64_t inter) {
     if (!moe_sizes_ok(tokens, topk, experts, hidden, inter)) return 0;
-    return moe_layout(tokens, topk, inter).total;
+    return moe_layout(tokens, topk, hidden, inter).total;
 }
 
 extern "C" int moe_forward_fp8_block(const void* x, const int* ids, const float* weights, int64_t tokens, int64_t topk,
@@ -1171,13 +1205,13 @@ extern "C" int moe_forward_fp8_block(const void* x, const int* ids, const float*
         if (workspace == nullptr) return fail(FP8DSA_ERR_INVALID_ARG, "workspace is required");
         if ((reinterpret_cast<uintptr_t>(workspace) & 255) != 0)
             return fail(FP8DSA_ERR_UNSUPPORTED, "workspace must be 256-byte aligned");
-        if (workspace_bytes < moe_layout(tokens, topk, inter).total)
+        if (workspace_bytes < moe_layout(tokens, topk, hidden, inter).total)
             return fail(FP8DSA_ERR_WORKSPACE, "workspace too small: see moe_forward_fp8_block_workspace_size");
     }
     int rc = check_device();
     if (rc) return rc;
     if (tokens == 0) return FP8DSA_OK;
-    const MoeLayout L = moe_layout(tokens, topk, inter);
+    const MoeLayout L = moe_layout(tokens, topk, hidden, inter);
     StreamArgs g{};
     g.idesc = (1u << 4) | (static_cast<uint32_t>(fmt) << 7) | (static_cast<uint32_t>(fmt) << 10) |
               (static_cast<uint32_t>(kBM >> 4) << 24);
@@ -1192,8 +1226,13 @@ extern "C" int moe_forward_fp8_block(const void* x, const int* ids, const float*
     g.inter = static_cast<int>(inter);
     g.hq = static_cast<uint8_t*>(workspace) + L.hq;
     g.sh = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + L.sh);
-    // at most `tokens` pairs of an expert unless a token names it twice: runs of 16 where that is enough and the
-    // tables leave room for two CTAs per SM
-    return tokens <= 16 && moe_fits<16>(g.tokens, g.pairs, g.experts) ? moe_launch<16>(g, w13, w13_scale, w2, w2_scale, x, out, stream)
-                        : moe_launch<32>(g, w13, w13_scale, w2, w2_scale, x, out, stream);
+    if (tokens > kQuantizeBefore) {
+        g.xq = static_cast<uint8_t*>(workspace) + L.xq;
+        g.sxq = reinterpret_cast<const float*>(static_cast<uint8_t*>(workspace) + L.sxq);
+    }
+    // Runs of 16 pairs (two CTAs per SM) where an expert has no more, or few experts do on average; an expert with
+    // more has its weights read again for every further run.
+    const bool few = tokens <= 16 || g.pairs <= 8 * g.experts;
+    return few && moe_fits<16>(g.tokens, g.pairs, g.experts) ? moe_launch<16>(g, w13, w13_scale, w2, w2_scale, x, out, stream)
+                                                             : moe_launch<32>(g, w13, w13_scale, w2, w2_scale, x, out, stream);
 }
