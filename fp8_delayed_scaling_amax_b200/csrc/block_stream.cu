@@ -98,7 +98,8 @@ struct StreamArgs {
     const int* ids;
     const float* weights;
     const float* w_scale;
-    int tokens, pairs, topk, experts, hidden, inter;
+    int tokens, pairs, experts, hidden, inter;
+    uint32_t topk_inv;          // 2^16 / topk, rounded up
     const uint8_t* xq;          // [tokens][hidden] quantized before (more than 16 tokens)
     const float* sxq;           // [blocks of hidden][tokens]
     uint8_t* hq;                // [pairs][inter]
@@ -107,9 +108,20 @@ struct StreamArgs {
     WaitCtl wait;
 };
 
-struct Entry {  // up to NMAX pairs of one expert
-    uint16_t expert, start, n, pad;
+struct Entry {  // up to kRun pairs of one expert
+    int expert, start, n;
 };
+// Runs of 16 with two CTAs per SM.  An expert with more pairs has its weights read again, mostly from L2, for
+// every further run: 61 tokens x 4 over 16 experts took 94 us so, and 132 us in runs of 32 with an SM to itself.
+constexpr int kRun = 16;
+// as stored: 10, 11 and 4 bits
+__device__ __forceinline__ uint32_t pack_entry(int expert, int start, int n) {
+    return static_cast<uint32_t>(expert | (start << 10) | ((n - 1) << 21));
+}
+__device__ __forceinline__ Entry unpack_entry(uint32_t v) {
+    return Entry{static_cast<int>(v & 1023u), static_cast<int>((v >> 10) & 2047u), static_cast<int>(v >> 21) + 1};
+}
+static_assert(FP8DSA_MOE_MAX_EXPERTS <= 1024 && FP8DSA_MOE_MAX_TOKENS * FP8DSA_MOE_MAX_TOPK <= 2048 && kRun <= 16, "entries");
 
 __device__ __forceinline__ void st_cluster_f32(uint32_t addr, float v) {
     asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
@@ -117,47 +129,46 @@ __device__ __forceinline__ void st_cluster_f32(uint32_t addr, float v) {
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 
-// Pairs sorted by expert (stable), and the entries: runs of at most nmax pairs of one expert.
+// Pairs sorted by expert (stable), and the entries: runs of at most kRun pairs of one expert.
 struct Table {
-    int* start;         // [experts] first sorted position (scratch before)
-    uint16_t* id;       // [pairs] expert or 0xFFFF
-    uint16_t* rank;     // [pairs] position among the expert's pairs
+    int* total;         // entries
     uint16_t* sorted;   // [pairs] the pair at a sorted position
-    uint16_t* token;    // [pairs] its token
+    uint32_t* entries;
     float* weight;      // [pairs] its weight (second launch)
-    Entry* entries;
-    int* total;
 };
 
-__host__ __device__ inline int max_entries(int pairs, int experts, int nmax) {
-    return (pairs < experts ? pairs : experts) + pairs / nmax;
+__host__ __device__ constexpr int max_entries(int pairs, int experts) {
+    return (pairs < experts ? pairs : experts) + pairs / kRun;
 }
-__host__ __device__ inline int table_bytes(int pairs, int experts, int nmax) {
+__host__ __device__ constexpr int table_bytes(int pairs, int experts, bool weights) {
     const int p8 = (pairs + 7) / 8 * 8;
-    return 16 + ((experts + 3) / 4 * 4) * 4 + 4 * p8 * 2 + p8 * 4 + max_entries(pairs, experts, nmax) * 8;
+    return 16 + p8 * 2 + (max_entries(pairs, experts) + 3) / 4 * 16 + (weights ? p8 * 4 : 0);
 }
 
 __device__ __forceinline__ Table table_at(uint8_t* base, const StreamArgs& g) {
     Table t;
-    const int p8 = (g.pairs + 7) / 8 * 8;
     t.total = reinterpret_cast<int*>(base);
-    t.start = reinterpret_cast<int*>(base + 16);
-    t.id = reinterpret_cast<uint16_t*>(t.start + (g.experts + 3) / 4 * 4);
-    t.rank = t.id + p8;
-    t.sorted = t.rank + p8;
-    t.token = t.sorted + p8;
-    t.weight = reinterpret_cast<float*>(t.token + p8);
-    t.entries = reinterpret_cast<Entry*>(t.weight + p8);
+    t.sorted = reinterpret_cast<uint16_t*>(base + 16);
+    t.entries = reinterpret_cast<uint32_t*>(t.sorted + (g.pairs + 7) / 8 * 8);
+    t.weight = reinterpret_cast<float*>(t.entries + (max_entries(g.pairs, g.experts) + 3) / 4 * 4);
     return t;
 }
 
-// Whole CTA.  Deterministic: ranks follow the pairs' order.  Ends with a barrier.
+// pair / topk: topk_inv is 2^16 / topk, rounded up, which is exact for up to 2048 pairs and 32 slots
+__device__ __forceinline__ int token_of(const StreamArgs& g, int pair) {
+    return static_cast<int>((static_cast<uint32_t>(pair) * g.topk_inv) >> 16);
+}
+
+// Whole CTA.  Deterministic: ranks follow the pairs' order.  `scratch` (build_scratch bytes) is the ring, which
+// nothing fills yet.  Ends with a barrier.
+constexpr int build_scratch(int threads) {
+    return threads / 32 * FP8DSA_MOE_MAX_EXPERTS * 2 + FP8DSA_MOE_MAX_EXPERTS * 4 + 2 * FP8DSA_MOE_MAX_TOKENS * FP8DSA_MOE_MAX_TOPK * 2;
+}
 template <bool kWeights, int kThreads>
-__device__ __forceinline__ void build_table(const Table& t, const StreamArgs& g, int nmax) {
+__device__ __forceinline__ void build_table(const Table& t, const StreamArgs& g, uint8_t* scratch) {
     const int tid = threadIdx.x, lane = tid & 31;
     auto place = [&](int pos, int p, float w) {
         t.sorted[pos] = static_cast<uint16_t>(p);
-        t.token[pos] = static_cast<uint16_t>(p / g.topk);
         if (kWeights) t.weight[pos] = w;
     };
     if (g.pairs <= 32) {
@@ -169,9 +180,9 @@ __device__ __forceinline__ void build_table(const Table& t, const StreamArgs& g,
             const uint32_t mask = __match_any_sync(0xFFFFFFFFu, valid ? e0 : -1);
             const uint32_t below = (1u << lane) - 1u;
             const int rank = __popc(mask & below);
-            const bool leader = valid && rank % nmax == 0;  // the first pair of an entry
+            const bool leader = valid && rank % kRun == 0;  // the first pair of an entry
             const uint32_t leaders = __ballot_sync(0xFFFFFFFFu, leader);
-            const int n = leader ? min(nmax, __popc(mask) - rank) : 0;
+            const int n = leader ? min(kRun, __popc(mask) - rank) : 0;
             int start = n;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -179,117 +190,89 @@ __device__ __forceinline__ void build_table(const Table& t, const StreamArgs& g,
                 if (lane >= o) start += v;
             }
             start -= n;
-            if (leader)
-                t.entries[__popc(leaders & below)] =
-                    Entry{static_cast<uint16_t>(e0), static_cast<uint16_t>(start), static_cast<uint16_t>(n), 0};
+            if (leader) t.entries[__popc(leaders & below)] = pack_entry(e0, start, n);
             // this pair's entry starts at the last leader of its expert up to itself
             const uint32_t mine = leaders & mask & (below | (1u << lane));
             const int from = __shfl_sync(0xFFFFFFFFu, start, valid ? 31 - __clz(mine) : lane);
-            if (valid) place(from + rank % nmax, lane, w);
+            if (valid) place(from + rank % kRun, lane, w);
             if (lane == 0) *t.total = __popc(leaders);
         }
         __syncthreads();
         return;
     }
-    if (g.pairs <= kThreads) {
-        // a thread per pair: its sorted position is the number of pairs of lower experts and of earlier pairs of
-        // its own, counted eight at a time from shared memory (two passes of pairs / 8 steps; sorting with one
-        // warp took 6500 cycles for 128 pairs)
-        const int p8 = (g.pairs + 7) / 8 * 8;
+    // Every warp ranks a run of consecutive pairs within itself and counts them by expert in a row of its own;
+    // then a thread per expert sums the rows, and one warp the experts.
+    // One warp ranking all pairs took 6500 cycles for 128 of them; counting, for each pair, the pairs before
+    // it took 20000 for 512.
+    constexpr int kWarps = kThreads / 32;
+    const int warp = tid >> 5, chunks = (g.pairs + 31) / 32, per = (chunks + kWarps - 1) / kWarps;
+    const int rows = (chunks + per - 1) / per, e4 = (g.experts + 3) / 4 * 4;
+    const int p_begin = warp * per * 32, p_end = min(g.pairs, p_begin + per * 32);
+    int* start = reinterpret_cast<int*>(scratch);                         // [experts] pairs, then the first position
+    uint16_t* counts = reinterpret_cast<uint16_t*>(start + e4);           // [warp][experts]
+    uint16_t* ids = counts + kWarps * e4;                                 // [pairs] expert or 0xFFFF
+    uint16_t* ranks = ids + FP8DSA_MOE_MAX_TOKENS * FP8DSA_MOE_MAX_TOPK;  // [pairs] position among its warp's
+    uint16_t* mine = counts + warp * e4;
+    for (int i = tid; i < rows * e4 / 2; i += kThreads) reinterpret_cast<uint32_t*>(counts)[i] = 0u;
+    __syncthreads();
+    for (int p0 = p_begin; p0 < p_end; p0 += 32) {
+        const int p = p0 + lane;
         uint32_t e = 0xFFFFu;
-        if (tid < p8) {
-            if (tid < g.pairs) {
-                const int v = __ldg(g.ids + tid);
-                if (v >= 0 && v < g.experts) e = static_cast<uint32_t>(v);
-            }
-            t.id[tid] = static_cast<uint16_t>(e);
+        if (p < p_end) {
+            const int v = __ldg(g.ids + p);
+            if (v >= 0 && v < g.experts) e = static_cast<uint32_t>(v);
+            ids[p] = static_cast<uint16_t>(e);
         }
-        const float w = kWeights && tid < g.pairs ? __ldg(g.weights + tid) : 0.0f;
-        __syncthreads();
-        int pos = 0, rank = 0, count = 0;
+        const uint32_t mask = __match_any_sync(0xFFFFFFFFu, e);
+        const int before = __popc(mask & ((1u << lane) - 1u));
+        int base = 0;
         if (e != 0xFFFFu) {
-            for (int q0 = 0; q0 < p8; q0 += 8) {
-                const uint4 v = *reinterpret_cast<const uint4*>(t.id + q0);
-                const uint32_t words[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    const uint32_t o = (words[k >> 1] >> (16 * (k & 1))) & 0xFFFFu;
-                    pos += o < e;
-                    count += o == e;
-                    rank += o == e && q0 + k < tid;
-                }
-            }
-            pos += rank;
+            base = mine[e];
+            ranks[p] = static_cast<uint16_t>(base + before);
         }
-        const bool leader = e != 0xFFFFu && rank % nmax == 0;  // the first pair of an entry
-        if (tid < p8) t.rank[tid] = leader ? static_cast<uint16_t>(pos) : 0xFFFFu;
-        if (e != 0xFFFFu) place(pos, tid, w);
-        const int leaders = __syncthreads_count(leader);
-        if (leader) {
-            int ent = 0;
-            for (int q0 = 0; q0 < p8; q0 += 8) {
-                const uint4 v = *reinterpret_cast<const uint4*>(t.rank + q0);
-                const uint32_t words[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-                for (int k = 0; k < 8; ++k) ent += ((words[k >> 1] >> (16 * (k & 1))) & 0xFFFFu) < static_cast<uint32_t>(pos);
-            }
-            t.entries[ent] = Entry{static_cast<uint16_t>(e), static_cast<uint16_t>(pos),
-                                   static_cast<uint16_t>(min(nmax, count - rank)), 0};
-        }
-        if (tid == 0) *t.total = leaders;
-        __syncthreads();
-        return;
+        __syncwarp();
+        if (e != 0xFFFFu && before == 0) mine[e] = static_cast<uint16_t>(base + __popc(mask));
+        __syncwarp();
     }
-    for (int e = tid; e < g.experts; e += kThreads) t.start[e] = 0;
-    for (int p = tid; p < g.pairs; p += kThreads) {
-        const int e = __ldg(g.ids + p);
-        t.id[p] = e >= 0 && e < g.experts ? static_cast<uint16_t>(e) : 0xFFFFu;
+    __syncthreads();
+    for (int e = tid; e < g.experts; e += kThreads) {
+        int run = 0;
+        for (int r = 0; r < rows; ++r) {
+            const int c = counts[r * e4 + e];
+            counts[r * e4 + e] = static_cast<uint16_t>(run);
+            run += c;
+        }
+        start[e] = run;
     }
     __syncthreads();
     if (tid < 32) {
-        for (int p0 = 0; p0 < g.pairs; p0 += 32) {
-            const int p = p0 + lane;
-            const uint32_t e = p < g.pairs ? t.id[p] : 0xFFFFu;
-            const uint32_t mask = __match_any_sync(0xFFFFFFFFu, e);
-            const int before = __popc(mask & ((1u << lane) - 1u));
-            int base = 0;
-            if (e != 0xFFFFu) {
-                base = t.start[e];
-                t.rank[p] = static_cast<uint16_t>(base + before);
-            }
-            __syncwarp();
-            if (e != 0xFFFFu && before == 0) t.start[e] = base + __popc(mask);
-            __syncwarp();
-        }
         int pos = 0, ent = 0;
         for (int e0 = 0; e0 < g.experts; e0 += 32) {
             const int e = e0 + lane;
-            const int c = e < g.experts ? t.start[e] : 0;
-            const int ne = (c + nmax - 1) / nmax;
-            int ci = c, ni = ne;
+            const int c = e < g.experts ? start[e] : 0;
+            const int ne = (c + kRun - 1) / kRun;
+            int both = c | (ne << 16);  // pairs and entries: 2048 each at most
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
-                const int a = __shfl_up_sync(0xFFFFFFFFu, ci, o), b = __shfl_up_sync(0xFFFFFFFFu, ni, o);
-                if (lane >= o) {
-                    ci += a;
-                    ni += b;
-                }
+                const int v = __shfl_up_sync(0xFFFFFFFFu, both, o);
+                if (lane >= o) both += v;
             }
-            const int first = pos + ci - c, ent0 = ent + ni - ne;
-            if (e < g.experts) t.start[e] = first;
+            const int first = pos + (both & 0xFFFF) - c, ent0 = ent + (both >> 16) - ne;
+            if (e < g.experts) start[e] = first;
             for (int q = 0; q < ne; ++q)
-                t.entries[ent0 + q] = Entry{static_cast<uint16_t>(e), static_cast<uint16_t>(first + q * nmax),
-                                            static_cast<uint16_t>(min(nmax, c - q * nmax)), 0};
-            pos += __shfl_sync(0xFFFFFFFFu, ci, 31);
-            ent += __shfl_sync(0xFFFFFFFFu, ni, 31);
+                t.entries[ent0 + q] = pack_entry(e, first + q * kRun, min(kRun, c - q * kRun));
+            const int all = __shfl_sync(0xFFFFFFFFu, both, 31);
+            pos += all & 0xFFFF;
+            ent += all >> 16;
         }
         if (lane == 0) *t.total = ent;
     }
     __syncthreads();
-    for (int p = tid; p < g.pairs; p += kThreads) {
-        const uint32_t e = t.id[p];
-        if (e != 0xFFFFu) place(t.start[e] + t.rank[p], p, kWeights ? __ldg(g.weights + p) : 0.0f);
+    for (int p = p_begin + lane; p < p_end; p += 32) {
+        const uint32_t e = ids[p];
+        if (e != 0xFFFFu) place(start[e] + mine[e] + ranks[p], p, kWeights ? __ldg(g.weights + p) : 0.0f);
     }
+    fence_proxy_async_smem();  // the ring is TMA's from here on
     __syncthreads();
 }
 
@@ -399,8 +382,8 @@ __global__ void __launch_bounds__(threads_of(NMAX), ctas_per_sm(NMAX))
     uint8_t* tail = smem + g.stages * kStage;
     // The scales' ring is twice as long: a stage is built again once its MMAs are done, when those of the unit
     // before that have been read.
-    float* xs = reinterpret_cast<float*>(tail);                // [2 kMaxStages][NMAX] the tokens' scales
-    float* ws = xs + 2 * kMaxStages * NMAX;                    // [2 kMaxStages][2] the weight tiles' scales
+    float* xs = reinterpret_cast<float*>(tail);                // [2 stages][NMAX] the tokens' scales
+    float* ws = xs + 2 * g.stages * NMAX;                      // [2 kMaxStages][2] the weight tiles' scales
     uint64_t* full = reinterpret_cast<uint64_t*>(ws + 4 * kMaxStages);  // weights landed and tokens written
     uint64_t* done = full + kMaxStages;                        // MMAs complete
     uint64_t* drain = done + kMaxStages;
@@ -439,7 +422,7 @@ __global__ void __launch_bounds__(threads_of(NMAX), ctas_per_sm(NMAX))
     Table table{};
     if constexpr (kMoe) {
         table = table_at(smem + g.off_table, g);
-        build_table<kMode == kDown, kThreads>(table, g, NMAX);
+        build_table<kMode == kDown, kThreads>(table, g, smem);
     }
     tc_fence_before_sync();
     __syncthreads();
@@ -476,7 +459,7 @@ __global__ void __launch_bounds__(threads_of(NMAX), ctas_per_sm(NMAX))
     // (first launch) item of cursor entry i: expert-major, so that CTAs side by side read one expert
     auto item_of = [&](int ent) { return cluster_id + ent * clusters; };
     auto tile_of = [&](int ent) { return kIsUp ? item_of(ent) % g.row_tiles : cluster_id % g.row_tiles; };
-    auto entry_at = [&](int ent) { return table.entries[kIsUp ? item_of(ent) / g.row_tiles : ent]; };
+    auto entry_at = [&](int ent) { return unpack_entry(table.entries[kIsUp ? item_of(ent) / g.row_tiles : ent]); };
     const int batch = kMoe ? 0 : cluster_id / g.row_tiles;
 
     if (warp == 0) {
@@ -533,7 +516,7 @@ __global__ void __launch_bounds__(threads_of(NMAX), ctas_per_sm(NMAX))
             for (int i = 0; i < units; ++i, c.advance(1, g.k_blocks)) {
                 if (c.ent != ent) {
                     ent = c.ent;
-                    const int n = kMoe ? static_cast<int>(entry_at(ent).n) : g.ncols;
+                    const int n = kMoe ? entry_at(ent).n : g.ncols;
                     idesc = g.idesc | (static_cast<uint32_t>((n + 15) / 16 * 2) << 17);  // N = n up to a multiple of 16
                 }
                 if (!ready && !mbar_wait_bounded(full + st, phase, g.wait, abort_flag, kStatusWaitMma)) break;
@@ -575,7 +558,7 @@ __global__ void __launch_bounds__(threads_of(NMAX), ctas_per_sm(NMAX))
         // FP8 rows come by TMA: only their scales are copied)
         constexpr int kRowsAtOnce = kQuant ? 2 : 4;
         constexpr int kUnroll = kMode == kDenseFp8 ? 1 : NMAX / 4;
-        static_assert(kQuant || kMode == kDenseFp8 || NMAX <= 32, "a copied tile is one batch");
+        static_assert(kQuant || kMode == kDenseFp8 || NMAX <= kRun, "a copied tile is one batch");
         constexpr int kBatch = kMode == kDenseFp8 ? NMAX : kRowsAtOnce * kUnroll;
         constexpr int kScales = kQuant ? 1 : (NMAX + 31) / 32;  // copying: scales per lane
         const int lrow = kQuant ? lane >> 4 : lane >> 3;        // row within kRowsAtOnce
@@ -585,7 +568,7 @@ __global__ void __launch_bounds__(threads_of(NMAX), ctas_per_sm(NMAX))
             uint4 v[kUnroll];
         } cur, nxt;
         float sc_cur[kScales], sw_cur = 0.0f;
-        auto columns = [&](int ent) { return kMoe ? static_cast<int>(entry_at(ent).n) : g.ncols; };
+        auto columns = [&](int ent) { return kMoe ? entry_at(ent).n : g.ncols; };
         auto load = [&](Cursor c, int n, int j0, Batch& out, float (&scale)[kScales], float& w_scale) {
             if (j0 == 0 && lane < kTiles) {
                 // the weight tile's scale (128 x 128 blocks), with the tokens': it may come from HBM, and the
@@ -596,7 +579,7 @@ __global__ void __launch_bounds__(threads_of(NMAX), ctas_per_sm(NMAX))
                 else if (g.sw.shift != 0)
                     w_scale = __ldg(g.sw.p + static_cast<int64_t>(tile_of(0)) * g.sw.s_mn + c.kb * g.sw.s_kb + batch * g.sw.s_b);
             }
-            const int pos = kMoe ? static_cast<int>(entry_at(c.ent).start) : 0;
+            const int pos = kMoe ? entry_at(c.ent).start : 0;
             const int64_t col = static_cast<int64_t>(c.kb) * kBK + lcol;
 #pragma unroll
             for (int r = 0; r < (kMode == kDenseFp8 ? 0 : kUnroll); ++r) {
@@ -605,7 +588,7 @@ __global__ void __launch_bounds__(threads_of(NMAX), ctas_per_sm(NMAX))
                 if (j >= n || col >= klen) continue;
                 if constexpr (kQuant) {
                     const uint16_t* row = static_cast<const uint16_t*>(g.x) +
-                                          (kMode == kUp ? table.token[pos + j] * g.ldx : batch * g.x_batch + j * g.ldx);
+                                          (kMode == kUp ? token_of(g, table.sorted[pos + j]) * g.ldx : batch * g.x_batch + j * g.ldx);
                     if (g.x_vec) {  // k % 8 == 0: the eight elements are all inside
                         out.v[r] = __ldg(reinterpret_cast<const uint4*>(row + col));
                     } else {
@@ -617,7 +600,7 @@ __global__ void __launch_bounds__(threads_of(NMAX), ctas_per_sm(NMAX))
                     }
                 } else {  // (hidden and inter are multiples of 16)
                     const uint8_t* row = kMode == kDown ? g.hq + static_cast<int64_t>(table.sorted[pos + j]) * g.inter
-                                                        : g.xq + static_cast<int64_t>(table.token[pos + j]) * g.hidden;
+                                                        : g.xq + static_cast<int64_t>(token_of(g, table.sorted[pos + j])) * g.hidden;
                     out.v[r] = __ldcg(reinterpret_cast<const uint4*>(row + col));
                 }
             }
@@ -630,7 +613,7 @@ __global__ void __launch_bounds__(threads_of(NMAX), ctas_per_sm(NMAX))
                         scale[q] = kMode == kDown
                                        ? __ldcg(g.sh + static_cast<int64_t>(c.kb) * g.pairs + table.sorted[pos + j])
                                    : kMode == kUpFp8
-                                       ? __ldcg(g.sxq + static_cast<int64_t>(c.kb) * g.tokens + table.token[pos + j])
+                                       ? __ldcg(g.sxq + static_cast<int64_t>(c.kb) * g.tokens + token_of(g, table.sorted[pos + j]))
                                        : __ldg(g.sx.p + static_cast<int64_t>(j >> g.sx.shift) * g.sx.s_mn + c.kb * g.sx.s_kb +
                                                batch * g.sx.s_b);
                 }
@@ -829,7 +812,7 @@ __global__ void __launch_bounds__(threads_of(NMAX), ctas_per_sm(NMAX))
 #pragma unroll
                         for (int k = 0; k < NMAX; ++k)
                             if (k == j) v = acc[0][k];
-                        float* dst = outacc + table.token[here.start + j] * kBM + row;
+                        float* dst = outacc + token_of(g, table.sorted[here.start + j]) * kBM + row;
                         *dst = fmaf(table.weight[here.start + j], v, *dst);
                     }
 #pragma unroll
@@ -982,9 +965,9 @@ cudaError_t kernel_setup() {
 // Shared memory: the ring, scales, barriers, then the table and `out_size` bytes (the second expert launch's
 // outputs, the first one's block maxima); as many stages as the budget and TMEM hold.
 template <int kMode, int NMAX>
-int stages_for(int table_size, int out_size) {
-    const int fixed = 2 * kMaxStages * NMAX * 4 + kBarBytes + static_cast<int>(align_up(static_cast<size_t>(table_size), 16)) + out_size;
-    const int n = std::min(max_stages(kMode, NMAX), (smem_budget(NMAX) - fixed) / stage_bytes(kMode, NMAX));
+constexpr int stages_for(int table_size, int out_size) {
+    const int n = std::min(max_stages(kMode, NMAX),
+                           (smem_budget(NMAX) - kBarBytes - table_size - out_size) / (stage_bytes(kMode, NMAX) + 2 * NMAX * 4));
     return n >= min_stages(NMAX) ? n : 0;
 }
 
@@ -993,13 +976,13 @@ int launch_stream(const CUtensorMap& map_w, const CUtensorMap& map_x, StreamArgs
                   cudaStream_t stream) {
     // the sums' exchange lies over the ring
     static_assert(min_stages(NMAX) * stage_bytes(kMode, NMAX) >= tiles_of(kMode) * NMAX * kBM * 4, "exchange");
+    static_assert(kMode < kUp || min_stages(NMAX) * stage_bytes(kMode, NMAX) >= build_scratch(threads_of(NMAX)), "table");
     static_assert(kMode != kDown || min_stages(NMAX) * stage_bytes(kMode, NMAX) >= FP8DSA_MOE_MAX_TOKENS * kBM * 4, "exchange");
     const cudaError_t se = kernel_setup<kMode, NMAX>();
     if (se != cudaSuccess) return fail(FP8DSA_ERR_CUDA, std::string("cudaFuncSetAttribute: ") + cudaGetErrorString(se));
     g.stages = stages_for<kMode, NMAX>(table_size, out_size);
-    if (g.stages == 0) return fail(FP8DSA_ERR_UNSUPPORTED, "shared memory: too many tokens, experts or slots");
-    g.off_table = g.stages * stage_bytes(kMode, NMAX) + 2 * kMaxStages * NMAX * 4 + kBarBytes;
-    g.off_out = g.off_table + static_cast<int>(align_up(static_cast<size_t>(table_size), 16));
+    g.off_table = g.stages * (stage_bytes(kMode, NMAX) + 2 * NMAX * 4) + kBarBytes;
+    g.off_out = g.off_table + table_size;
     const int rc = wait_ctl(&g.wait);
     if (rc) return rc;
     const cudaError_t e = launch_ex(block_stream_kernel<kMode, NMAX>, dim3(static_cast<unsigned>(grid)), dim3(threads_of(NMAX)),
@@ -1098,19 +1081,19 @@ bool moe_sizes_ok(int64_t tokens, int64_t topk, int64_t experts, int64_t hidden,
            hidden >= 16 && inter >= 16 && hidden % 16 == 0 && inter % 16 == 0 && hidden <= (1 << 24) && inter <= (1 << 24);
 }
 
-// More tokens than this are quantized by a launch of their own.
+// More tokens than this are quantized by a launch of their own: it costs one token 2.3 us, and sixteen nothing;
+// without it 61 tokens took 150 us instead of 132.
 constexpr int64_t kQuantizeBefore = 16;
 
-constexpr int kMaximaBytes = 2 * 4 * 32 * 4;  // two items, four warps, up to 32 columns
+constexpr int kMaximaBytes = 2 * 4 * kRun * 4;  // two items, four warps
 
-// Whether both launches of an instance fit in shared memory.
-template <int NMAX>
-bool moe_fits(int tokens, int pairs, int experts) {
-    const int table = table_bytes(pairs, experts, NMAX);
-    return stages_for<kUpFp8, NMAX>(table, kMaximaBytes) > 0 && stages_for<kDown, NMAX>(table, tokens * kBM * 4) > 0;
+// The largest tables fit beside the smallest ring.
+constexpr int table_bytes_max(bool weights) {
+    return table_bytes(FP8DSA_MOE_MAX_TOKENS * FP8DSA_MOE_MAX_TOPK, FP8DSA_MOE_MAX_EXPERTS, weights);
 }
+static_assert(stages_for<kUp, kRun>(table_bytes_max(false), kMaximaBytes) > 0, "shared memory");
+static_assert(stages_for<kDown, kRun>(table_bytes_max(true), FP8DSA_MOE_MAX_TOKENS * kBM * 4) > 0, "shared memory");
 
-template <int NMAX>
 int moe_launch(StreamArgs g, const uint8_t* w13, const float* w13_scale, const uint8_t* w2, const float* w2_scale,
                const void* x, void* out, cudaStream_t stream) {
     const int hb = (g.hidden + kBK - 1) / kBK, ib = (g.inter + kBK - 1) / kBK;
@@ -1122,8 +1105,8 @@ int moe_launch(StreamArgs g, const uint8_t* w13, const float* w13_scale, const u
     rc = encode_tensor_map(&m2, u8, w2, g.inter, g.hidden, g.experts, g.inter, static_cast<int64_t>(g.hidden) * g.inter, 128,
                            128, CU_TENSOR_MAP_SWIZZLE_128B);
     if (rc) return rc;
-    const int entries = max_entries(g.pairs, g.experts, NMAX);
-    const int table = table_bytes(g.pairs, g.experts, NMAX);
+    const int entries = max_entries(g.pairs, g.experts);
+    const int table = table_bytes(g.pairs, g.experts, false);
     const double row_flops = 2.0 * g.pairs * static_cast<double>(g.hidden) * g.inter;
 
     StreamArgs a = g;
@@ -1145,12 +1128,12 @@ int moe_launch(StreamArgs g, const uint8_t* w13, const float* w13_scale, const u
     a.row_tiles = ib;
     a.w_scale = w13_scale;
     // `entries` is the most there can be; without clusters as many CTAs as run at once walk what there is
-    a.splits = split_for(static_cast<int64_t>(entries) * ib, hb, ctas_per_sm(NMAX));
+    a.splits = split_for(static_cast<int64_t>(entries) * ib, hb, ctas_per_sm(kRun));
     int64_t grid = static_cast<int64_t>(entries) * ib * a.splits;
-    if (a.splits == 1) grid = std::min<int64_t>(grid, static_cast<int64_t>(ctas_per_sm(NMAX)) * sm_count());
+    if (a.splits == 1) grid = std::min<int64_t>(grid, static_cast<int64_t>(ctas_per_sm(kRun)) * sm_count());
     launch_begin(kKindGemm, stream);
-    rc = g.xq != nullptr ? launch_stream<kUpFp8, NMAX>(m13, m13, a, table, kMaximaBytes, grid, stream)
-                         : launch_stream<kUp, NMAX>(m13, m13, a, table, kMaximaBytes, grid, stream);
+    rc = g.xq != nullptr ? launch_stream<kUpFp8, kRun>(m13, m13, a, table, kMaximaBytes, grid, stream)
+                         : launch_stream<kUp, kRun>(m13, m13, a, table, kMaximaBytes, grid, stream);
     if (rc) return rc;
     launch_end(kKindGemmSingle, stream, 2.0 * row_flops);
 
@@ -1161,9 +1144,9 @@ int moe_launch(StreamArgs g, const uint8_t* w13, const float* w13_scale, const u
     b.out = static_cast<uint16_t*>(out);
     b.ldo = g.hidden;
     b.out_vec = (reinterpret_cast<uintptr_t>(out) & 7) == 0;
-    b.splits = split_for(hb, static_cast<int64_t>(std::min(g.pairs, g.experts)) * ib, ctas_per_sm(NMAX));
+    b.splits = split_for(hb, static_cast<int64_t>(std::min(g.pairs, g.experts)) * ib, ctas_per_sm(kRun));
     launch_begin(kKindGemm, stream);
-    rc = launch_stream<kDown, NMAX>(m2, m2, b, table, g.tokens * kBM * 4, static_cast<int64_t>(hb) * b.splits, stream);
+    rc = launch_stream<kDown, kRun>(m2, m2, b, table_bytes(g.pairs, g.experts, true), g.tokens * kBM * 4, static_cast<int64_t>(hb) * b.splits, stream);
     if (rc) return rc;
     launch_end(kKindGemmSingle, stream, row_flops);
     return check_launch("block stream kernel");
@@ -1219,7 +1202,7 @@ extern "C" int moe_forward_fp8_block(const void* x, const int* ids, const float*
     g.ids = ids;
     g.weights = weights;
     g.tokens = static_cast<int>(tokens);
-    g.topk = static_cast<int>(topk);
+    g.topk_inv = static_cast<uint32_t>((65536 + topk - 1) / topk);
     g.pairs = static_cast<int>(tokens * topk);
     g.experts = static_cast<int>(experts);
     g.hidden = static_cast<int>(hidden);
@@ -1230,9 +1213,5 @@ extern "C" int moe_forward_fp8_block(const void* x, const int* ids, const float*
         g.xq = static_cast<uint8_t*>(workspace) + L.xq;
         g.sxq = reinterpret_cast<const float*>(static_cast<uint8_t*>(workspace) + L.sxq);
     }
-    // Runs of 16 pairs (two CTAs per SM) where an expert has no more, or few experts do on average; an expert with
-    // more has its weights read again for every further run.
-    const bool few = tokens <= 16 || g.pairs <= 8 * g.experts;
-    return few && moe_fits<16>(g.tokens, g.pairs, g.experts) ? moe_launch<16>(g, w13, w13_scale, w2, w2_scale, x, out, stream)
-                                                             : moe_launch<32>(g, w13, w13_scale, w2, w2_scale, x, out, stream);
+    return moe_launch(g, w13, w13_scale, w2, w2_scale, x, out, stream);
 }

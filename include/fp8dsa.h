@@ -498,7 +498,8 @@ int linear_backward_fp8_block(const void* g, const uint8_t* x8c, const float* x8
 size_t moe_forward_fp8_block_workspace_size(int64_t tokens, int64_t topk, int64_t experts, int64_t hidden,
                                             int64_t inter);
 
-/* Mixture-of-experts feed-forward layer for a few tokens (decoding), block-scaled FP8, two launches:
+/* Mixture-of-experts feed-forward layer for a few tokens (decoding), block-scaled FP8, two launches (three
+ * for more than 16 tokens, which are quantized first):
  *   for every token t and slot s with 0 <= e = ids[t][s] < experts (other ids: the slot is skipped; an
  *   expert may be named more than once, and a token without any valid slot gives a zero row):
  *       (g, u) = q(x[t]) . w13[e]^T         q: fp8_quantize_block, 1 x 128 blocks, in fmt

@@ -118,6 +118,13 @@ def test_moe_matches_fp64(tokens, topk, experts, hidden, inter):
     check(tokens, topk, experts, hidden, inter, seed=tokens + hidden)
 
 
+@pytest.mark.parametrize("tokens,topk,experts,hidden,inter", [
+    (64, 32, 1024, 32, 48), (64, 8, 64, 256, 144), (11, 32, 100, 128, 128), (64, 32, 33, 128, 128), (64, 1, 1000, 64, 128)])
+def test_moe_large_tables(tokens, topk, experts, hidden, inter):
+    """The most pairs and experts there can be, and pairs that several warps rank in several steps each."""
+    check(tokens, topk, experts, hidden, inter, seed=experts)
+
+
 def test_moe_e5m2_and_unaligned_rows():
     check(4, 2, 4, 256, 256, fmt="e5m2", seed=3)
     check(6, 2, 4, 272, 256, seed=4, x_shift=1)
