@@ -138,12 +138,14 @@ def header_functions():
 
 
 def _ptr(t):
-    if t is None:
-        return None
+    if t is None or type(t) is int:
+        return t
+    try:
+        return t.data_ptr()
+    except AttributeError:
+        pass
     if isinstance(t, int):
         return t
-    if hasattr(t, "data_ptr"):
-        return t.data_ptr()
     raise TypeError(f"expected a tensor, an int pointer or None, got {type(t)}")
 
 
@@ -360,25 +362,13 @@ def linear_backward_fp8_saved_t(g, x8t, w8t, m, k, n, fmt, fmt_t, need_grad_x, n
         _stream(stream)))
 
 
-class BlockScale:
-    """Host description of a block-scaled operand's scales (``fp8_block_scale_t``): the fp32 tensor
-    and its strides in elements; ``block_mn`` is 1 (a scale per row) or 128."""
+class BlockScale(fp8_block_scale_t):
+    """A block-scaled operand's scales: the fp32 tensor (kept alive as ``tensor``) and its strides in
+    elements; ``block_mn`` is 1 (a scale per row) or 128."""
 
     def __init__(self, scale, block_mn: int, stride_mn: int, stride_kb: int, stride_batch: int = 0):
-        self.scale = scale
-        self.block_mn = int(block_mn)
-        self.stride_mn = int(stride_mn)
-        self.stride_kb = int(stride_kb)
-        self.stride_batch = int(stride_batch)
-
-    def as_c(self) -> fp8_block_scale_t:
-        return fp8_block_scale_t(_ptr(self.scale), self.block_mn, self.stride_mn, self.stride_kb, self.stride_batch)
-
-
-def _block_scale(s):
-    if s is None:
-        return None
-    return ctypes.byref(s if isinstance(s, fp8_block_scale_t) else s.as_c())
+        super().__init__(_ptr(scale), block_mn, stride_mn, stride_kb, stride_batch)
+        self.tensor = scale
 
 
 def fp8_quantize_block(x, in_type, rows, cols, fmt, out_row, scale_row, out_col=None, scale_col=None, stream=None):
@@ -399,7 +389,7 @@ def fp8_gemm_block(a, b, fmt_a, fmt_b, layout, m, n, k, lda, ldb, ldo, batch, st
     """Product of block-scaled operands; scale_a / scale_b are :class:`BlockScale`."""
     return _check("fp8_gemm_block", lib().fp8_gemm_block(
         _ptr(a), _ptr(b), int(fmt_a), int(fmt_b), int(layout), int(m), int(n), int(k), int(lda), int(ldb), int(ldo),
-        int(batch), int(stride_a), int(stride_b), int(stride_o), _block_scale(scale_a), _block_scale(scale_b),
+        int(batch), int(stride_a), int(stride_b), int(stride_o), scale_a, scale_b,
         _ptr(bias), _ptr(out), _stream(stream)))
 
 
