@@ -12,8 +12,8 @@
 //  * a ring of stages, each a 128 x 128 weight tile (gate and up: two), a token tile, its scales and a TMEM
 //    buffer: warp 0 streams the weights by TMA, warp 1 issues the MMAs, three to five warps build the
 //    token tiles (FP8 rows come by TMA, the experts' hidden rows are copied, bf16 rows quantized on the
-//    way: 1 x 128 blocks never leave a tile) and fetch the scales, four add the blocks with their scales
-//    in fp32 registers (a thread owns one weight row).  One commit per stage frees it for the producer
+//    way: 1 x 128 blocks never leave a tile) and fetch the scales, four or eight add the blocks with their
+//    scales in fp32 registers (a thread owns one weight row).  One commit per stage frees it for the producer
 //    and hands it to the adders.  Rings and commits of their own for weights, tokens and TMEM took the
 //    issuer 1200 to 1600 cycles a unit, more than a unit's bytes take from HBM.
 //  * two CTAs per SM for up to 16 tokens: 100 to 190 KB per SM are in flight;
@@ -43,7 +43,6 @@ constexpr int kBK = 128;       // K per block
 constexpr int kUmmaK = 32;
 constexpr int kTileBytes = kBM * kBK;
 constexpr int kFirstBuilder = 2;
-constexpr int kEpiThreads = 128;
 constexpr int kMaxStages = 12;
 constexpr int kBarBytes = 512;
 constexpr int kMaxSplit = 8;
@@ -58,7 +57,10 @@ constexpr int ctas_per_sm(int nmax) { return nmax == 16 ? 2 : 1; }
 constexpr int smem_budget(int nmax) { return ctas_per_sm(nmax) == 2 ? 112 * 1024 : 224 * 1024; }
 constexpr int tmem_cols(int nmax) { return 512 / ctas_per_sm(nmax); }
 constexpr int builders(int nmax) { return nmax == 16 ? 3 : 5; }
-constexpr int threads_of(int nmax) { return 32 * (kFirstBuilder + builders(nmax)) + kEpiThreads; }
+// Four adders, one per quarter of the weight rows; of 64 columns each of eight takes 32.  (With four, 64 columns'
+// adders took 1050 cycles a unit, twice what its bytes take, mostly to fetch their unrolled code the first time.)
+constexpr int adders(int nmax) { return nmax == 16 ? 4 : 8; }
+constexpr int threads_of(int nmax) { return 32 * (kFirstBuilder + builders(nmax) + adders(nmax)); }
 // A builder waits for a stage's last use without having seen the uses between.  Units complete in order (one
 // thread issues all MMAs, and a unit's builder arrives before it), so with at least as many stages as
 // builders none of them can be a whole phase behind or ahead of a barrier.
@@ -366,11 +368,13 @@ struct Cursor {
     }
 };
 
+// (the experts' modes have 16 columns and four adders)
 template <int kMode, int NMAX>
 __global__ void __launch_bounds__(threads_of(NMAX), ctas_per_sm(NMAX))
     block_stream_kernel(const __grid_constant__ CUtensorMap tma_w, const __grid_constant__ CUtensorMap tma_x,
                         const __grid_constant__ StreamArgs g) {
     constexpr int kBuilders = builders(NMAX), kFirstEpi = kFirstBuilder + kBuilders, kThreads = threads_of(NMAX);
+    constexpr int kAdders = adders(NMAX), kOwn = 4 * NMAX / kAdders;  // kOwn: columns per adder
     constexpr bool kIsUp = is_up(kMode);
     constexpr bool kMoe = kIsUp || kMode == kDown;
     constexpr int kTiles = kIsUp ? 2 : 1;   // weight tiles per K block (gate and up)
@@ -398,14 +402,14 @@ __global__ void __launch_bounds__(threads_of(NMAX), ctas_per_sm(NMAX))
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < R; ++i) {
-            mbar_init(full + i, 6);  // the weights, the tokens, and the four adders of the unit a ring ago
+            mbar_init(full + i, 2 + kAdders);  // the weights, the tokens, and the adders of the unit a ring ago
             mbar_init(done + i, 2);  // the MMAs' commit, and the builder (whose scales the adders read)
         }
         mbar_init(drain, 1);
         *abort_flag = 0;
         fence_mbar_init();
         for (int i = 0; i < R; ++i)
-            for (int w = 0; w < 4; ++w) mbar_arrive(full + i);  // nothing is there to be added at first
+            for (int w = 0; w < kAdders; ++w) mbar_arrive(full + i);  // nothing is there to be added at first
         prefetch_tensormap(&tma_w);
     }
     if (warp == 1) {
@@ -696,11 +700,12 @@ __global__ void __launch_bounds__(threads_of(NMAX), ctas_per_sm(NMAX))
         constexpr int kAtOnce = kTiles == 1 ? 2 : 1;
         const int q = warp & 3;
         const int row = q * 32 + lane;               // of the tile
-        float acc[kTiles][NMAX];
+        const int col0 = kOwn == NMAX ? 0 : (warp - kFirstEpi) / 4 * kOwn;
+        float acc[kTiles][kOwn];
 #pragma unroll
         for (int t = 0; t < kTiles; ++t)
 #pragma unroll
-            for (int j = 0; j < NMAX; ++j) acc[t][j] = 0.0f;
+            for (int j = 0; j < kOwn; ++j) acc[t][j] = 0.0f;
         int n = g.ncols;
         Entry en{};
         auto enter = [&](int ent) {
@@ -747,7 +752,7 @@ __global__ void __launch_bounds__(threads_of(NMAX), ctas_per_sm(NMAX))
                         if (row_scales) sw_row = ldg_pinned(sw_at + c.kb * g.sw.s_kb);
                     }
                     // (scales and sums come with `done`)  A warp that gave up runs on without waiting or adding, so
-                    // that the barrier at the end of an item still finds all four.
+                    // that the barrier at the end of an item still finds all of them.
                     if (ok) ok = mbar_wait_bounded(done + st, phase, g.wait, abort_flag, kStatusWaitEpilogue);
                     if (++st == R) {
                         st = 0;
@@ -766,8 +771,8 @@ __global__ void __launch_bounds__(threads_of(NMAX), ctas_per_sm(NMAX))
 #pragma unroll
                     for (int t = 0; t < kTiles; ++t) sw[p][t] = row_scales ? u_sw[p] : ws[2 * u_slot[p] + t];
 #pragma unroll
-                for (int cc = 0; cc < NMAX; cc += 16) {
-                    if (cc >= n_here) break;
+                for (int cc = 0; cc < kOwn; cc += 16) {
+                    if (col0 + cc >= n_here) break;
                     // two units side by side, or a unit's two tiles one after the other (registers)
 #pragma unroll
                     for (int t = 0; t < kTiles; ++t) {
@@ -775,12 +780,12 @@ __global__ void __launch_bounds__(threads_of(NMAX), ctas_per_sm(NMAX))
 #pragma unroll
                         for (int p = 0; p < kAtOnce; ++p)
                             if (p < count)
-                                tmem_load_16cols(tmem_mine + static_cast<uint32_t>((u_st[p] * kTiles + t) * NMAX + cc), d[p]);
+                                tmem_load_16cols(tmem_mine + static_cast<uint32_t>((u_st[p] * kTiles + t) * NMAX + col0 + cc), d[p]);
                         tmem_wait_ld();
 #pragma unroll
                         for (int p = 0; p < kAtOnce; ++p) {
                             if (p < count) {
-                                const float* sc = xs + u_slot[p] * NMAX + cc;  // columns from n on: never stored
+                                const float* sc = xs + u_slot[p] * NMAX + col0 + cc;  // columns from n on: never stored
 #pragma unroll
                                 for (int e = 0; e < 16; e += 4) {
                                     const float4 f = *reinterpret_cast<const float4*>(sc + e);
@@ -845,7 +850,7 @@ __global__ void __launch_bounds__(threads_of(NMAX), ctas_per_sm(NMAX))
                         const float am = warp_max(fabsf(h));
                         if (lane == 0) most[q * NMAX + j] = am;
                     }
-                    named_barrier(1, kEpiThreads);
+                    named_barrier(1, 32 * kAdders);
 #pragma unroll 1
                     for (int j = 0; j < here.n; ++j) {
                         float h = 0.0f;
@@ -888,8 +893,8 @@ __global__ void __launch_bounds__(threads_of(NMAX), ctas_per_sm(NMAX))
                 const int per = kBM / g.splits, own = row / per;
                 const uint32_t at = mapa_shared(recv + static_cast<uint32_t>(rank * g.ncols * per + row % per) * 4, own);
 #pragma unroll
-                for (int j = 0; j < NMAX; ++j)
-                    if (j < g.ncols) st_cluster_f32(at + static_cast<uint32_t>(j * per) * 4, acc[0][j]);
+                for (int j = 0; j < kOwn; ++j)
+                    if (col0 + j < g.ncols) st_cluster_f32(at + static_cast<uint32_t>((col0 + j) * per) * 4, acc[0][j]);
             }
         }
         if constexpr (kMode == kDown) {  // (zeros, too, from a CTA that had no unit)
