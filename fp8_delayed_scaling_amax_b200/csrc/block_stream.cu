@@ -368,6 +368,29 @@ struct Cursor {
     }
 };
 
+// Column j of packed sums, by comparison (indexing would put them in memory).
+template <int kPairs>
+__device__ __forceinline__ float column(const uint64_t (&acc)[kPairs], int j) {
+    float v = 0.0f;
+#pragma unroll
+    for (int k = 0; k < kPairs; ++k) {
+        float lo, hi;
+        unpack_f32x2(acc[k], lo, hi);
+        if (2 * k == j) v = lo;
+        if (2 * k + 1 == j) v = hi;
+    }
+    return v;
+}
+template <int kPairs>
+__device__ __forceinline__ void set_column(uint64_t (&acc)[kPairs], int j, float v) {
+#pragma unroll
+    for (int k = 0; k < kPairs; ++k) {
+        float lo, hi;
+        unpack_f32x2(acc[k], lo, hi);
+        acc[k] = pack_f32x2(2 * k == j ? v : lo, 2 * k + 1 == j ? v : hi);
+    }
+}
+
 // (the experts' modes have 16 columns and four adders)
 template <int kMode, int NMAX>
 __global__ void __launch_bounds__(threads_of(NMAX), ctas_per_sm(NMAX))
@@ -694,169 +717,154 @@ __global__ void __launch_bounds__(threads_of(NMAX), ctas_per_sm(NMAX))
         cluster_wait();
     } else {
         // ------------------------------------------------------------------ blocks added with their scales
-        // Two units at a time where one weight tile makes a unit: a unit's barrier, TMEM load and hand-back are
-        // mostly latency (800 cycles one by one, which bounded the second expert launch).  Loops over columns
-        // outside the K loop are rolled: little code, little of it fetched.
+        // Two sums at a time: two units of one weight tile each, or a unit's gate and up.  A round is mostly latency
+        // (1500 cycles with a wait per unit, the scales read after the sums and a cursor moved unit by unit),
+        // so the two barriers are looked at together and the scales are multiplied while TMEM is read.  Loops over
+        // columns outside the K loop are rolled: little code, little of it fetched.
         constexpr int kAtOnce = kTiles == 1 ? 2 : 1;
         const int q = warp & 3;
         const int row = q * 32 + lane;               // of the tile
         const int col0 = kOwn == NMAX ? 0 : (warp - kFirstEpi) / 4 * kOwn;
-        float acc[kTiles][kOwn];
+        const uint32_t tmem_mine = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(col0);
+        uint64_t acc2[kTiles][kOwn / 2];             // pairs of columns
 #pragma unroll
         for (int t = 0; t < kTiles; ++t)
 #pragma unroll
-            for (int j = 0; j < kOwn; ++j) acc[t][j] = 0.0f;
-        int n = g.ncols;
-        Entry en{};
-        auto enter = [&](int ent) {
-            if constexpr (kMoe) {
-                en = entry_at(ent);
-                n = en.n;
-            }
-        };
-        // a product whose weight has a scale per row: this thread's, loaded a block ahead
+            for (int j = 0; j < kOwn / 2; ++j) acc2[t][j] = 0u;
+        // a product whose weight has a scale per row: this thread's, loaded a round ahead
         const bool row_scales = !kMoe && g.sw.shift == 0;
         const float* sw_at = nullptr;
-        float sw_row = 0.0f;
+        float sw_row[2] = {0.0f, 0.0f};
         Cursor c = first(0);
-        if (units > 0) {
-            enter(c.ent);
-            if (row_scales) {
-                const int grow = min(tile_of(0) * kBM + row, g.rows - 1);  // rows past the end are never stored
-                sw_at = g.sw.p + static_cast<int64_t>(grow) * g.sw.s_mn + batch * g.sw.s_b;
-                sw_row = ldg_pinned(sw_at + c.kb * g.sw.s_kb);
-            }
+        if (row_scales && units > 0) {
+            const int grow = min(tile_of(0) * kBM + row, g.rows - 1);  // rows past the end are never stored
+            sw_at = g.sw.p + static_cast<int64_t>(grow) * g.sw.s_mn + batch * g.sw.s_b + c.kb * g.sw.s_kb;
+#pragma unroll
+            for (int p = 0; p < 2; ++p)
+                if (p < units) sw_row[p] = ldg_pinned(sw_at + p * g.sw.s_kb);
         }
-        int st = 0, slot = 0;
+        int st = 0, slot = 0, n = g.ncols;
         uint32_t phase = 0;
         bool ok = true;
         for (int i = 0; i < units;) {
-            // the units of this round: one, or two of the same entry
-            int u_st[kAtOnce], u_slot[kAtOnce], count = 0;
-            float u_sw[kAtOnce];
-            bool ends = false;  // the entry (or this CTA's part of it) is complete with the round
-            const int ent = c.ent, n_here = n;
-            const Entry here = en;
-#pragma unroll
-            for (int p = 0; p < kAtOnce; ++p) {
-                u_st[p] = st;
-                u_slot[p] = slot;
-                u_sw[p] = sw_row;
-                if (i < units && !ends) {
-                    ++i;
-                    ++count;
-                    c.advance(1, g.k_blocks);
-                    ends = i == units || c.ent != ent;
-                    if (i < units) {
-                        if (ends) enter(c.ent);
-                        if (row_scales) sw_row = ldg_pinned(sw_at + c.kb * g.sw.s_kb);
-                    }
-                    // (scales and sums come with `done`)  A warp that gave up runs on without waiting or adding, so
-                    // that the barrier at the end of an item still finds all of them.
-                    if (ok) ok = mbar_wait_bounded(done + st, phase, g.wait, abort_flag, kStatusWaitEpilogue);
-                    if (++st == R) {
-                        st = 0;
-                        phase ^= 1u;
-                    }
-                    if (++slot == 2 * R) slot = 0;
-                }
+            // the units of one entry (or this CTA's part of them)
+            const int ent = c.ent, len = min(units - i, g.k_blocks - c.kb);
+            Entry here{};
+            if constexpr (kMoe) {
+                here = entry_at(ent);
+                n = here.n;
             }
-            ok = __all_sync(0xFFFFFFFFu, ok);
-            if (ok) {
-                tc_fence_after_sync();
-                const uint32_t tmem_mine = tmem_base + (static_cast<uint32_t>(q * 32) << 16);
-                float sw[kAtOnce][kTiles];
+            for (int r = 0; r < len; r += kAtOnce) {
+                const bool two = kAtOnce == 2 && r + 1 < len;
+                int st1 = st, slot1 = slot;
+                uint32_t phase1 = phase;
+                if (two) {
+                    if (++st1 == R) {
+                        st1 = 0;
+                        phase1 ^= 1u;
+                    }
+                    if (++slot1 == 2 * R) slot1 = 0;
+                }
+                // (scales and sums come with `done`)  A warp that gave up runs on without waiting or adding, so that
+                // the barrier at the end of an item still finds all of them.
+                if (ok) {
+                    const bool done0 = mbar_test_wait(done + st, phase), done1 = mbar_test_wait(done + st1, phase1);
+                    if (!(done0 && done1))
+                        ok = mbar_wait_bounded(done + st, phase, g.wait, abort_flag, kStatusWaitEpilogue) &&
+                             mbar_wait_bounded(done + st1, phase1, g.wait, abort_flag, kStatusWaitEpilogue);
+                }
+                ok = __all_sync(0xFFFFFFFFu, ok);
+                if (ok) {
+                    tc_fence_after_sync();
+                    float sw0 = ws[2 * slot], sw1 = ws[kTiles == 2 ? 2 * slot + 1 : 2 * slot1];
+                    if (row_scales) {
+                        sw0 = sw_row[0];
+                        sw1 = sw_row[1];
 #pragma unroll
-                for (int p = 0; p < kAtOnce; ++p)
+                        for (int p = 0; p < 2; ++p)
+                            if (r + 2 + p < len) sw_row[p] = ldg_pinned(sw_at + (r + 2 + p) * g.sw.s_kb);
+                    }
+                    const uint64_t sw_pair[2] = {pack_f32x2(sw0, sw0), pack_f32x2(sw1, sw1)};
+                    const uint32_t sum0 = tmem_mine + static_cast<uint32_t>(st * kTiles * NMAX);
+                    const uint32_t sum1 = kTiles == 2 ? sum0 + NMAX : tmem_mine + static_cast<uint32_t>(st1 * NMAX);
+                    const float* sc0 = xs + slot * NMAX + col0;  // columns from n on: never stored
+                    const float* sc1 = kTiles == 2 ? sc0 : xs + slot1 * NMAX + col0;
 #pragma unroll
-                    for (int t = 0; t < kTiles; ++t) sw[p][t] = row_scales ? u_sw[p] : ws[2 * u_slot[p] + t];
+                    for (int cc = 0; cc < kOwn; cc += 16) {
+                        if (col0 + cc >= n) break;
+                        uint32_t d0[16], d1[16];
+                        tmem_load_16cols(sum0 + cc, d0);
+                        tmem_load_16cols(sum1 + cc, d1);
+                        uint64_t f0[8], f1[8];
 #pragma unroll
-                for (int cc = 0; cc < kOwn; cc += 16) {
-                    if (col0 + cc >= n_here) break;
-                    // two units side by side, or a unit's two tiles one after the other (registers)
-#pragma unroll
-                    for (int t = 0; t < kTiles; ++t) {
-                        uint32_t d[kAtOnce][16];
-#pragma unroll
-                        for (int p = 0; p < kAtOnce; ++p)
-                            if (p < count)
-                                tmem_load_16cols(tmem_mine + static_cast<uint32_t>((u_st[p] * kTiles + t) * NMAX + col0 + cc), d[p]);
+                        for (int e = 0; e < 8; e += 2) {
+                            const float4 a = *reinterpret_cast<const float4*>(sc0 + cc + 2 * e);
+                            const float4 b = *reinterpret_cast<const float4*>(sc1 + cc + 2 * e);
+                            f0[e] = mul_f32x2(sw_pair[0], pack_f32x2(a.x, a.y));
+                            f0[e + 1] = mul_f32x2(sw_pair[0], pack_f32x2(a.z, a.w));
+                            f1[e] = mul_f32x2(sw_pair[1], pack_f32x2(b.x, b.y));
+                            f1[e + 1] = mul_f32x2(sw_pair[1], pack_f32x2(b.z, b.w));
+                        }
                         tmem_wait_ld();
 #pragma unroll
-                        for (int p = 0; p < kAtOnce; ++p) {
-                            if (p < count) {
-                                const float* sc = xs + u_slot[p] * NMAX + col0 + cc;  // columns from n on: never stored
+                        for (int e = 0; e < 8; ++e) fma_f32x2(acc2[0][cc / 2 + e], pack_b32x2(d0[2 * e], d0[2 * e + 1]), f0[e]);
+                        if (two || kTiles == 2) {
 #pragma unroll
-                                for (int e = 0; e < 16; e += 4) {
-                                    const float4 f = *reinterpret_cast<const float4*>(sc + e);
-                                    float* at = &acc[t][cc + e];
-                                    at[0] = fmaf(__uint_as_float(d[p][e]), __fmul_rn(sw[p][t], f.x), at[0]);
-                                    at[1] = fmaf(__uint_as_float(d[p][e + 1]), __fmul_rn(sw[p][t], f.y), at[1]);
-                                    at[2] = fmaf(__uint_as_float(d[p][e + 2]), __fmul_rn(sw[p][t], f.z), at[2]);
-                                    at[3] = fmaf(__uint_as_float(d[p][e + 3]), __fmul_rn(sw[p][t], f.w), at[3]);
-                                }
-                            }
+                            for (int e = 0; e < 8; ++e)
+                                fma_f32x2(acc2[kTiles - 1][cc / 2 + e], pack_b32x2(d1[2 * e], d1[2 * e + 1]), f1[e]);
                         }
                     }
+                    // the stages' sums and scales are read
+                    tc_fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0) {
+                        mbar_arrive(full + st);
+                        if (two) mbar_arrive(full + st1);
+                    }
                 }
-                // the stages' sums and scales are read
-                tc_fence_before_sync();
-                __syncwarp();
-                if (lane == 0) {
-#pragma unroll
-                    for (int p = 0; p < kAtOnce; ++p)
-                        if (p < count) mbar_arrive(full + u_st[p]);
+                st = st1 + 1;
+                phase = phase1;
+                if (st == R) {
+                    st = 0;
+                    phase ^= 1u;
                 }
+                slot = slot1 + 1 == 2 * R ? 0 : slot1 + 1;
             }
+            i += len;
+            ++c.ent;
+            c.kb = 0;
             if constexpr (kMode == kDown) {
                 // add the entry to its tokens' rows, which only this thread touches
-                if (ends) {
 #pragma unroll 1
-                    for (int j = 0; j < here.n; ++j) {
-                        float v = 0.0f;
-#pragma unroll
-                        for (int k = 0; k < NMAX; ++k)
-                            if (k == j) v = acc[0][k];
-                        float* dst = outacc + token_of(g, table.sorted[here.start + j]) * kBM + row;
-                        *dst = fmaf(table.weight[here.start + j], v, *dst);
-                    }
-#pragma unroll
-                    for (int k = 0; k < NMAX; ++k) acc[0][k] = 0.0f;
+                for (int j = 0; j < n; ++j) {
+                    const float v = column(acc2[0], j);
+                    const int at = here.start + j;
+                    float* dst = outacc + token_of(g, table.sorted[at]) * kBM + row;
+                    *dst = fmaf(table.weight[at], v, *dst);
                 }
+#pragma unroll
+                for (int k = 0; k < kOwn / 2; ++k) acc2[0][k] = 0u;
             }
             if constexpr (kIsUp) {
                 // Without a cluster the item is complete here: a thread has its row's gate and up sums, the
                 // block's maximum goes over the four warps.
-                if (ends && g.splits == 1) {
+                if (g.splits == 1) {
                     float* most = reinterpret_cast<float*>(smem + g.off_out) + (ent & 1) * 4 * NMAX;  // [warp][column]
                     const int tile = tile_of(ent), at = tile * kBM + row;
                     // Rolled loops that pick a column's registers by comparison: this code runs once per item, and
                     // unrolled it took 25000 cycles the first time, nearly all of them instruction fetches from
                     // a memory system that is busy with weights.
 #pragma unroll 1
-                    for (int j = 0; j < here.n; ++j) {
-                        float gate = 0.0f, up = 0.0f;
-#pragma unroll
-                        for (int k = 0; k < NMAX; ++k) {
-                            if (k == j) {
-                                gate = acc[0][k];
-                                up = acc[1][k];
-                            }
-                        }
-                        const float h = at < g.inter ? gated(gate, up) : 0.0f;
-#pragma unroll
-                        for (int k = 0; k < NMAX; ++k)
-                            if (k == j) acc[0][k] = h;
+                    for (int j = 0; j < n; ++j) {
+                        const float h = at < g.inter ? gated(column(acc2[0], j), column(acc2[1], j)) : 0.0f;
+                        set_column(acc2[0], j, h);
                         const float am = warp_max(fabsf(h));
                         if (lane == 0) most[q * NMAX + j] = am;
                     }
                     named_barrier(1, 32 * kAdders);
 #pragma unroll 1
-                    for (int j = 0; j < here.n; ++j) {
-                        float h = 0.0f;
-#pragma unroll
-                        for (int k = 0; k < NMAX; ++k)
-                            if (k == j) h = acc[0][k];
+                    for (int j = 0; j < n; ++j) {
+                        const float h = column(acc2[0], j);
                         const float am = fmaxf(fmaxf(most[j], most[NMAX + j]), fmaxf(most[2 * NMAX + j], most[3 * NMAX + j]));
                         const float s = block_step(am, g.fmt);
                         const float v = __fmul_rn(h, __frcp_rn(s));
@@ -866,10 +874,15 @@ __global__ void __launch_bounds__(threads_of(NMAX), ctas_per_sm(NMAX))
                         if (row == 0) g.sh[static_cast<int64_t>(tile) * g.pairs + p] = s;
                     }
 #pragma unroll
-                    for (int j = 0; j < NMAX; ++j) acc[0][j] = acc[1][j] = 0.0f;
+                    for (int j = 0; j < kOwn / 2; ++j) acc2[0][j] = acc2[1][j] = 0u;
                 }
             }
         }
+        float acc[kTiles][kOwn];
+#pragma unroll
+        for (int t = 0; t < kTiles; ++t)
+#pragma unroll
+            for (int j = 0; j < kOwn / 2; ++j) unpack_f32x2(acc2[t][j], acc[t][2 * j], acc[t][2 * j + 1]);
         // Once every CTA of the cluster is through with its ring, the sums go (over the rings) to the CTAs that
         // write them out: rows to row / (128 / splits), or a pair's h (which needs its whole block) to
         // column % splits.
