@@ -107,6 +107,7 @@ struct StreamArgs {
     uint8_t* hq;                // [pairs][inter]
     float* sh;                  // [blocks of inter][pairs]
     int off_table, off_out;     // byte offsets in shared memory
+    int off_recv;               // of the cluster's sums; 0: over the ring
     WaitCtl wait;
 };
 
@@ -161,13 +162,32 @@ __device__ __forceinline__ int token_of(const StreamArgs& g, int pair) {
     return static_cast<int>((static_cast<uint32_t>(pair) * g.topk_inv) >> 16);
 }
 
+// The pairs are dealt to the warps in runs; a thread's first one, loaded before the table is built (a load takes 3000
+// cycles while the first launch streams its weights).
+struct FirstPair {
+    int id;
+    float weight;
+};
+__device__ __forceinline__ int pairs_per_warp(const StreamArgs& g, int warps) { return ((g.pairs + 31) / 32 + warps - 1) / warps * 32; }
+template <bool kWeights, int kThreads>
+__device__ __forceinline__ FirstPair load_first(const StreamArgs& g) {
+    const int run = pairs_per_warp(g, kThreads / 32);
+    const int p = static_cast<int>(threadIdx.x >> 5) * run + static_cast<int>(threadIdx.x & 31);
+    FirstPair f{-1, 0.0f};
+    if (p < g.pairs) {
+        f.id = __ldg(g.ids + p);
+        if (kWeights) f.weight = __ldg(g.weights + p);
+    }
+    return f;
+}
+
 // Whole CTA.  Deterministic: ranks follow the pairs' order.  `scratch` (build_scratch bytes) is the ring, which
 // nothing fills yet.  Ends with a barrier.
 constexpr int build_scratch(int threads) {
     return threads / 32 * FP8DSA_MOE_MAX_EXPERTS * 2 + FP8DSA_MOE_MAX_EXPERTS * 4 + 2 * FP8DSA_MOE_MAX_TOKENS * FP8DSA_MOE_MAX_TOPK * 2;
 }
 template <bool kWeights, int kThreads>
-__device__ __forceinline__ void build_table(const Table& t, const StreamArgs& g, uint8_t* scratch) {
+__device__ __forceinline__ void build_table(const Table& t, const StreamArgs& g, uint8_t* scratch, const FirstPair& first) {
     const int tid = threadIdx.x, lane = tid & 31;
     auto place = [&](int pos, int p, float w) {
         t.sorted[pos] = static_cast<uint16_t>(p);
@@ -176,8 +196,7 @@ __device__ __forceinline__ void build_table(const Table& t, const StreamArgs& g,
     if (g.pairs <= 32) {
         // one warp, in registers; entries in the order of their first pair
         if (tid < 32) {
-            const int e0 = lane < g.pairs ? __ldg(g.ids + lane) : -1;
-            const float w = kWeights && lane < g.pairs ? __ldg(g.weights + lane) : 0.0f;
+            const int e0 = first.id;
             const bool valid = e0 >= 0 && e0 < g.experts;
             const uint32_t mask = __match_any_sync(0xFFFFFFFFu, valid ? e0 : -1);
             const uint32_t below = (1u << lane) - 1u;
@@ -196,7 +215,7 @@ __device__ __forceinline__ void build_table(const Table& t, const StreamArgs& g,
             // this pair's entry starts at the last leader of its expert up to itself
             const uint32_t mine = leaders & mask & (below | (1u << lane));
             const int from = __shfl_sync(0xFFFFFFFFu, start, valid ? 31 - __clz(mine) : lane);
-            if (valid) place(from + rank % kRun, lane, w);
+            if (valid) place(from + rank % kRun, lane, first.weight);
             if (lane == 0) *t.total = __popc(leaders);
         }
         __syncthreads();
@@ -207,9 +226,9 @@ __device__ __forceinline__ void build_table(const Table& t, const StreamArgs& g,
     // One warp ranking all pairs took 6500 cycles for 128 of them; counting, for each pair, the pairs before
     // it took 20000 for 512.
     constexpr int kWarps = kThreads / 32;
-    const int warp = tid >> 5, chunks = (g.pairs + 31) / 32, per = (chunks + kWarps - 1) / kWarps;
-    const int rows = (chunks + per - 1) / per, e4 = (g.experts + 3) / 4 * 4;
-    const int p_begin = warp * per * 32, p_end = min(g.pairs, p_begin + per * 32);
+    const int warp = tid >> 5, run = pairs_per_warp(g, kWarps);
+    const int rows = (g.pairs + run - 1) / run, e4 = (g.experts + 3) / 4 * 4;
+    const int p_begin = warp * run, p_end = min(g.pairs, p_begin + run);
     int* start = reinterpret_cast<int*>(scratch);                         // [experts] pairs, then the first position
     uint16_t* counts = reinterpret_cast<uint16_t*>(start + e4);           // [warp][experts]
     uint16_t* ids = counts + kWarps * e4;                                 // [pairs] expert or 0xFFFF
@@ -217,11 +236,12 @@ __device__ __forceinline__ void build_table(const Table& t, const StreamArgs& g,
     uint16_t* mine = counts + warp * e4;
     for (int i = tid; i < rows * e4 / 2; i += kThreads) reinterpret_cast<uint32_t*>(counts)[i] = 0u;
     __syncthreads();
+    int next = first.id;
     for (int p0 = p_begin; p0 < p_end; p0 += 32) {
-        const int p = p0 + lane;
+        const int p = p0 + lane, v = next;
         uint32_t e = 0xFFFFu;
+        if (p + 32 < p_end) next = __ldg(g.ids + p + 32);
         if (p < p_end) {
-            const int v = __ldg(g.ids + p);
             if (v >= 0 && v < g.experts) e = static_cast<uint32_t>(v);
             ids[p] = static_cast<uint16_t>(e);
         }
@@ -238,13 +258,13 @@ __device__ __forceinline__ void build_table(const Table& t, const StreamArgs& g,
     }
     __syncthreads();
     for (int e = tid; e < g.experts; e += kThreads) {
-        int run = 0;
+        int before = 0;
         for (int r = 0; r < rows; ++r) {
             const int c = counts[r * e4 + e];
-            counts[r * e4 + e] = static_cast<uint16_t>(run);
-            run += c;
+            counts[r * e4 + e] = static_cast<uint16_t>(before);
+            before += c;
         }
-        start[e] = run;
+        start[e] = before;
     }
     __syncthreads();
     if (tid < 32) {
@@ -272,7 +292,7 @@ __device__ __forceinline__ void build_table(const Table& t, const StreamArgs& g,
     __syncthreads();
     for (int p = p_begin + lane; p < p_end; p += 32) {
         const uint32_t e = ids[p];
-        if (e != 0xFFFFu) place(start[e] + mine[e] + ranks[p], p, kWeights ? __ldg(g.weights + p) : 0.0f);
+        if (e != 0xFFFFu) place(start[e] + mine[e] + ranks[p], p, !kWeights ? 0.0f : p < p_begin + 32 ? first.weight : __ldg(g.weights + p));
     }
     fence_proxy_async_smem();  // the ring is TMA's from here on
     __syncthreads();
@@ -368,6 +388,11 @@ struct Cursor {
     }
 };
 
+// (first launch) the columns of an entry that one CTA of the cluster forms h of, at most
+__host__ __device__ __forceinline__ int own_columns(const StreamArgs& g, int split_log) {
+    return ((g.pairs < kRun ? g.pairs : kRun) + (1 << split_log) - 1) >> split_log;
+}
+
 // Column j of packed sums, by comparison (indexing would put them in memory).
 template <int kPairs>
 __device__ __forceinline__ float column(const uint64_t (&acc)[kPairs], int j) {
@@ -423,17 +448,23 @@ __global__ void __launch_bounds__(threads_of(NMAX), ctas_per_sm(NMAX))
     const int R = g.stages;
     if constexpr (!kIsUp) pdl_trigger();
 
-    if (threadIdx.x == 0) {
-        for (int i = 0; i < R; ++i) {
-            mbar_init(full + i, 2 + kAdders);  // the weights, the tokens, and the adders of the unit a ring ago
-            mbar_init(done + i, 2);  // the MMAs' commit, and the builder (whose scales the adders read)
+    // The second expert launch reads only ids and weights before its wait: the first one has waited for
+    // whatever wrote them before it let this launch start.
+    FirstPair mine{-1, 0.0f};
+    if constexpr (kMode == kDown) mine = load_first<true, kThreads>(g);
+    if (warp == 0) {
+        if (lane < R) {  // (thread 0 for all of them took 600 cycles)
+            mbar_init(full + lane, 2 + kAdders);  // the weights, the tokens, and the adders of the unit a ring ago
+            mbar_init(done + lane, 2);  // the MMAs' commit, and the builder (whose scales the adders read)
+            fence_mbar_init();
+            mbar_arrive_many(full + lane, kAdders);  // nothing is there to be added at first
         }
-        mbar_init(drain, 1);
-        *abort_flag = 0;
-        fence_mbar_init();
-        for (int i = 0; i < R; ++i)
-            for (int w = 0; w < kAdders; ++w) mbar_arrive(full + i);  // nothing is there to be added at first
-        prefetch_tensormap(&tma_w);
+        if (lane == 0) {
+            mbar_init(drain, 1);
+            *abort_flag = 0;
+            fence_mbar_init();
+            prefetch_tensormap(&tma_w);
+        }
     }
     if (warp == 1) {
         tmem_alloc(tmem_slot, kCols);
@@ -442,19 +473,25 @@ __global__ void __launch_bounds__(threads_of(NMAX), ctas_per_sm(NMAX))
     float* outacc = reinterpret_cast<float*>(smem + g.off_out);  // second launch: [tokens][128]
     if constexpr (kMode == kDown)
         for (int i = threadIdx.x; i < g.tokens * kBM; i += kThreads) outacc[i] = 0.0f;
-    // The second expert launch reads only ids and weights before its wait: the first one has waited for
-    // whatever wrote them before it let this launch start.
     if constexpr (kMode != kDown) pdl_wait();
-    if constexpr (kIsUp) pdl_trigger();
+    if constexpr (kIsUp) {
+        pdl_trigger();
+        mine = load_first<false, kThreads>(g);
+    }
     Table table{};
     if constexpr (kMoe) {
         table = table_at(smem + g.off_table, g);
-        build_table<kMode == kDown, kThreads>(table, g, smem);
+        build_table<kMode == kDown, kThreads>(table, g, smem, mine);
     }
     tc_fence_before_sync();
     __syncthreads();
     tc_fence_after_sync();
     const uint32_t tmem_base = *tmem_slot;
+    // Where the sums of the cluster's CTAs come to lie: over the ring, once every CTA is through with its own, or apart,
+    // where a peer only has to have started.
+    const bool apart = g.off_recv != 0;
+    const int split_log = 31 - __clz(g.splits);  // splits is 1, 2, 4 or 8
+    if (apart) cluster_arrive();
 
     // This CTA's units.  A cluster takes one item (a 128-row tile of the product, of one entry's gate and up,
     // or of the second launch's outputs) and cuts its units over its CTAs; without clusters the first
@@ -531,7 +568,7 @@ __global__ void __launch_bounds__(threads_of(NMAX), ctas_per_sm(NMAX))
                         break;
         }
         __syncwarp();
-        cluster_arrive();
+        if (!apart) cluster_arrive();
         cluster_wait();
     } else if (warp == 1) {
         // ------------------------------------------------------------------ MMA issuer
@@ -573,7 +610,7 @@ __global__ void __launch_bounds__(threads_of(NMAX), ctas_per_sm(NMAX))
             mbar_wait_bounded(drain, 0, g.wait, nullptr, kStatusWaitDrain);
         }
         __syncwarp();
-        cluster_arrive();
+        if (!apart) cluster_arrive();
         cluster_wait();
     } else if (warp < kFirstEpi) {
         // ------------------------------------------------------------------ token tiles
@@ -713,7 +750,7 @@ __global__ void __launch_bounds__(threads_of(NMAX), ctas_per_sm(NMAX))
             if (slot >= 2 * R) slot -= 2 * R;
         }
         __syncwarp();
-        cluster_arrive();
+        if (!apart) cluster_arrive();
         cluster_wait();
     } else {
         // ------------------------------------------------------------------ blocks added with their scales
@@ -883,37 +920,37 @@ __global__ void __launch_bounds__(threads_of(NMAX), ctas_per_sm(NMAX))
         for (int t = 0; t < kTiles; ++t)
 #pragma unroll
             for (int j = 0; j < kOwn / 2; ++j) unpack_f32x2(acc2[t][j], acc[t][2 * j], acc[t][2 * j + 1]);
-        // Once every CTA of the cluster is through with its ring, the sums go (over the rings) to the CTAs that
-        // write them out: rows to row / (128 / splits), or a pair's h (which needs its whole block) to
+        // The sums go to the CTAs of the cluster that write them out: rows to row / (128 / splits), or a pair's h (which needs its whole block) to
         // column % splits.
         __syncwarp();
-        cluster_arrive();
+        if (!apart) cluster_arrive();
         cluster_wait();
         if (ok && units > 0 && !(kIsUp && g.splits == 1)) {
-            const uint32_t recv = smem_addr(smem);
+            const uint32_t recv = smem_addr(smem + g.off_recv);
             if constexpr (kIsUp) {  // [range][tile][own column][row]
-                const int per = NMAX / g.splits;
+                const int per = own_columns(g, split_log);
 #pragma unroll
                 for (int j = 0; j < NMAX; ++j) {
-                    if (j < n) {
-                        const int own = j % g.splits, at = (rank * kTiles * per + j / g.splits) * kBM + row;
+                    if (j >= n) break;
+                    const int own = j & (g.splits - 1), at = (rank * kTiles * per + (j >> split_log)) * kBM + row;
 #pragma unroll
-                        for (int t = 0; t < kTiles; ++t)
-                            st_cluster_f32(mapa_shared(recv + static_cast<uint32_t>(at + t * per * kBM) * 4, own), acc[t][j]);
-                    }
+                    for (int t = 0; t < kTiles; ++t)
+                        st_cluster_f32(mapa_shared(recv + static_cast<uint32_t>(at + t * per * kBM) * 4, own), acc[t][j]);
                 }
             } else if constexpr (kMode != kDown) {  // [range][column][own row]
-                const int per = kBM / g.splits, own = row / per;
-                const uint32_t at = mapa_shared(recv + static_cast<uint32_t>(rank * g.ncols * per + row % per) * 4, own);
+                const int per = kBM >> split_log, own = row >> (7 - split_log);
+                const uint32_t at = mapa_shared(recv + static_cast<uint32_t>(rank * g.ncols * per + (row & (per - 1))) * 4, own);
 #pragma unroll
-                for (int j = 0; j < kOwn; ++j)
-                    if (col0 + j < g.ncols) st_cluster_f32(at + static_cast<uint32_t>((col0 + j) * per) * 4, acc[0][j]);
+                for (int j = 0; j < kOwn; ++j) {
+                    if (col0 + j >= g.ncols) break;
+                    st_cluster_f32(at + static_cast<uint32_t>((col0 + j) * per) * 4, acc[0][j]);
+                }
             }
         }
         if constexpr (kMode == kDown) {  // (zeros, too, from a CTA that had no unit)
-            const int per = kBM / g.splits, own = row / per;
-            const uint32_t at = mapa_shared(smem_addr(smem) +
-                                            static_cast<uint32_t>(rank * g.tokens * per + row % per) * 4, own);
+            const int per = kBM >> split_log, own = row >> (7 - split_log);
+            const uint32_t at = mapa_shared(smem_addr(smem + g.off_recv) +
+                                            static_cast<uint32_t>(rank * g.tokens * per + (row & (per - 1))) * 4, own);
             for (int j = 0; j < g.tokens; ++j) st_cluster_f32(at + static_cast<uint32_t>(j * per) * 4, outacc[j * kBM + row]);
         }
     }
@@ -922,22 +959,22 @@ __global__ void __launch_bounds__(threads_of(NMAX), ctas_per_sm(NMAX))
     __syncwarp();
     cluster_arrive();
     cluster_wait();  // every range's sums are here; nothing of this CTA's is read or written by a peer after it
-    const float* recv = reinterpret_cast<const float*>(smem);
+    const float* recv = reinterpret_cast<const float*>(smem + g.off_recv);
     if constexpr (kIsUp) {
         if (items > 0 && g.splits > 1) {
             const Entry en = entry_at(0);
-            const int per = NMAX / g.splits;
+            const int per = own_columns(g, split_log);
             for (int jj = warp; jj * g.splits + rank < en.n; jj += kThreads / 32)
                 form_h(g, recv, g.splits, kTiles * per * kBM, per * kBM, jj, table.sorted[en.start + jj * g.splits + rank],
                        tile_of(0), lane);
         }
     } else {
         // this CTA's rows of the tile for every column (product) or token (experts), four rows per item
-        const int per = kBM / g.splits, quads = per / 4;  // splits is 1, 2, 4 or 8
+        const int per = kBM >> split_log, quad_log = 5 - split_log;
         const int cols = kMode == kDown ? g.tokens : g.ncols;
         const int rows = kMode == kDown ? g.hidden : g.rows;
-        for (int i = threadIdx.x; i < cols * quads; i += kThreads) {
-            const int j = i / quads, r = 4 * (i % quads);
+        for (int i = threadIdx.x; i < cols << quad_log; i += kThreads) {
+            const int j = i >> quad_log, r = 4 * (i & ((1 << quad_log) - 1));
             const int row = tile_of(0) * kBM + rank * per + r;
             if (row >= rows) continue;
             float v[4] = {};
@@ -990,21 +1027,32 @@ constexpr int stages_for(int table_size, int out_size) {
 }
 
 template <int kMode, int NMAX>
-int launch_stream(const CUtensorMap& map_w, const CUtensorMap& map_x, StreamArgs& g, int table_size, int out_size, int64_t grid,
-                  cudaStream_t stream) {
+int launch_stream(const CUtensorMap& map_w, const CUtensorMap& map_x, StreamArgs& g, int table_size, int out_size,
+                  int64_t units, int64_t grid, cudaStream_t stream) {
     // the sums' exchange lies over the ring
     static_assert(min_stages(NMAX) * stage_bytes(kMode, NMAX) >= tiles_of(kMode) * NMAX * kBM * 4, "exchange");
     static_assert(kMode < kUp || min_stages(NMAX) * stage_bytes(kMode, NMAX) >= build_scratch(threads_of(NMAX)), "table");
     static_assert(kMode != kDown || min_stages(NMAX) * stage_bytes(kMode, NMAX) >= FP8DSA_MOE_MAX_TOKENS * kBM * 4, "exchange");
     const cudaError_t se = kernel_setup<kMode, NMAX>();
     if (se != cudaSuccess) return fail(FP8DSA_ERR_CUDA, std::string("cudaFuncSetAttribute: ") + cudaGetErrorString(se));
+    const int split_log = g.splits == 8 ? 3 : g.splits == 4 ? 2 : g.splits - 1;
+    const int recv = (kMode == kDown ? g.tokens : is_up(kMode) ? tiles_of(kMode) * own_columns(g, split_log) * g.splits : g.ncols) * kBM * 4;
+    // no more stages than a CTA has units; the sums' room apart, where that does not cost a stage (one token
+    // 4.9 -> 4.4 us)
     g.stages = stages_for<kMode, NMAX>(table_size, out_size);
+    g.stages = static_cast<int>(std::max<int64_t>(min_stages(NMAX), std::min<int64_t>(g.stages, units)));
     g.off_table = g.stages * (stage_bytes(kMode, NMAX) + 2 * NMAX * 4) + kBarBytes;
     g.off_out = g.off_table + table_size;
+    size_t bytes = static_cast<size_t>(g.off_out + out_size);
+    g.off_recv = 0;
+    if (bytes + static_cast<size_t>(recv) <= static_cast<size_t>(smem_budget(NMAX))) {
+        g.off_recv = static_cast<int>(bytes);
+        bytes += static_cast<size_t>(recv);
+    }
     const int rc = wait_ctl(&g.wait);
     if (rc) return rc;
     const cudaError_t e = launch_ex(block_stream_kernel<kMode, NMAX>, dim3(static_cast<unsigned>(grid)), dim3(threads_of(NMAX)),
-                                    static_cast<size_t>(g.off_out + out_size), stream, g.splits, map_w, map_x, g);
+                                    bytes, stream, g.splits, map_w, map_x, g);
     if (e != cudaSuccess) return fail(FP8DSA_ERR_CUDA, std::string("block stream launch: ") + cudaGetErrorString(e));
     return FP8DSA_OK;
 }
@@ -1063,14 +1111,14 @@ int block_stream_gemm(const BlockGemmDesc& d, bool x_is_bf16, cudaStream_t strea
     g.ldo = d.ldo;
     g.stride_o = d.stride_o;
     g.out_vec = (reinterpret_cast<uintptr_t>(d.out) & 7) == 0 && d.ldo % 4 == 0 && (d.batch == 1 || d.stride_o % 4 == 0);
-    const int64_t grid = tiles * g.splits;
+    const int64_t grid = tiles * g.splits, units = (g.k_blocks + g.splits - 1) / g.splits;
     launch_begin(kKindGemm, stream);
     if (x_is_bf16)
-        rc = launch_stream<kDenseBf16, 16>(map, map, g, 0, 0, grid, stream);
+        rc = launch_stream<kDenseBf16, 16>(map, map, g, 0, 0, units, grid, stream);
     else if (d.m <= 16)
-        rc = launch_stream<kDenseFp8, 16>(map, map_x, g, 0, 0, grid, stream);
+        rc = launch_stream<kDenseFp8, 16>(map, map_x, g, 0, 0, units, grid, stream);
     else
-        rc = launch_stream<kDenseFp8, 64>(map, map_x, g, 0, 0, grid, stream);
+        rc = launch_stream<kDenseFp8, 64>(map, map_x, g, 0, 0, units, grid, stream);
     if (rc) return rc;
     launch_end(kKindGemmSingle, stream, 2.0 * static_cast<double>(d.m) * d.n * d.k * d.batch);
     return check_launch("block stream kernel");
@@ -1149,9 +1197,10 @@ int moe_launch(StreamArgs g, const uint8_t* w13, const float* w13_scale, const u
     a.splits = split_for(static_cast<int64_t>(entries) * ib, hb, ctas_per_sm(kRun));
     int64_t grid = static_cast<int64_t>(entries) * ib * a.splits;
     if (a.splits == 1) grid = std::min<int64_t>(grid, static_cast<int64_t>(ctas_per_sm(kRun)) * sm_count());
+    int64_t units = a.splits > 1 ? (hb + a.splits - 1) / a.splits : int64_t(entries) * ib * hb;  // of a CTA, at most
     launch_begin(kKindGemm, stream);
-    rc = g.xq != nullptr ? launch_stream<kUpFp8, kRun>(m13, m13, a, table, kMaximaBytes, grid, stream)
-                         : launch_stream<kUp, kRun>(m13, m13, a, table, kMaximaBytes, grid, stream);
+    rc = g.xq != nullptr ? launch_stream<kUpFp8, kRun>(m13, m13, a, table, kMaximaBytes, units, grid, stream)
+                         : launch_stream<kUp, kRun>(m13, m13, a, table, kMaximaBytes, units, grid, stream);
     if (rc) return rc;
     launch_end(kKindGemmSingle, stream, 2.0 * row_flops);
 
@@ -1164,7 +1213,9 @@ int moe_launch(StreamArgs g, const uint8_t* w13, const float* w13_scale, const u
     b.out_vec = (reinterpret_cast<uintptr_t>(out) & 7) == 0;
     b.splits = split_for(hb, static_cast<int64_t>(std::min(g.pairs, g.experts)) * ib, ctas_per_sm(kRun));
     launch_begin(kKindGemm, stream);
-    rc = launch_stream<kDown, kRun>(m2, m2, b, table_bytes(g.pairs, g.experts, true), g.tokens * kBM * 4, static_cast<int64_t>(hb) * b.splits, stream);
+    units = (int64_t(entries) * ib + b.splits - 1) / b.splits;
+    rc = launch_stream<kDown, kRun>(m2, m2, b, table_bytes(g.pairs, g.experts, true), g.tokens * kBM * 4, units,
+                                  static_cast<int64_t>(hb) * b.splits, stream);
     if (rc) return rc;
     launch_end(kKindGemmSingle, stream, row_flops);
     return check_launch("block stream kernel");
