@@ -11,8 +11,9 @@
 // Structure (as the per-tensor GEMM, whose helpers it shares):
 //  * warp 0 = TMA producer, warps 1 and 2 = MMA issuers, 8 warps promote and write the output;
 //  * a stage holds one K block (128 bytes) of both operands; each K block goes to a TMEM buffer of its
-//    own (accumulate = 0 for its first MMA), handed over with one commit; the promotion of block b overlaps the MMAs of the blocks after it.  The tile's fp32 sums live in registers for the
-//    whole K loop: 128 per thread for 256-wide tiles.
+//    own (accumulate = 0 for its first MMA), handed over with one commit; the promotion of block b
+//    overlaps the MMAs of the blocks after it.  The tile's fp32 sums live in registers for the whole K
+//    loop: 128 per thread for 256-wide tiles.
 //  * 256 x 256 tiles on CTA pairs (M = 256 MMA across two SMs, each SM loads half of B), or
 //    128 x 128 tiles on single CTAs, which may split K over a cluster of up to 8 CTAs, whose sums are
 //    added through distributed shared memory in a fixed order (no workspace, no atomics).  A model
@@ -22,6 +23,13 @@
 //    the product sa * sb is one more; with sb per column each promotion warp keeps its own columns'
 //    scales of the current block in shared memory and reads them back as broadcasts.
 //  * every wait is bounded, as in the per-tensor GEMM.
+//
+// Bound by the promotion: a 256 x 256 pair block takes 950 cycles with one scale per thread and 1500 with
+// a scale per column (a multiply more for each sum), its MMAs 512.  Measured: 8192^3 537 to 557 us (2000
+// TFLOP/s; the tensor pipe is 55% busy at 4096^3, 70 us), 8192^3 with a scale per column on both sides 797 us.
+// Tried there and slower: a TMEM load shape that gives a thread four rows and a quarter of the columns, with
+// a quarter of the reads of the scales (4096^3 107 -> 110 us); the next block's first sums loaded before
+// the last ones are added (spills 54 registers: 70 -> 107 us).
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <cuda_bf16.h>

@@ -1,14 +1,16 @@
 // Block-scaled products of a few rows: the weight streams through once and the tensor cores take it as
 // the M operand (128 weight rows per tile), the tokens as N (16 to 64 columns).  Serves
 //   fp8_gemm_block / linear_forward_fp8_block with at most 64 rows, and
-//   moe_forward_fp8_block: a mixture-of-experts layer for at most 64 tokens, in two launches.
+//   moe_forward_fp8_block: a mixture-of-experts layer for at most 64 tokens, in two launches (more than 16
+//   tokens are quantized by one before).
 //
 //     product:  out[j][i] = RN_bf16( sum_b RN32(sw(i,b) sx(j,b)) (sum_{k in b} W[i][k] x[j][k]) + bias[i] )
 //     experts:  for every (token t, slot s) with e = ids[t][s] in 0 .. experts - 1:
 //                 g, u = rows of W13[e] . q(x[t]);  h = g / (1 + exp(-g)) * u  (fp32);  hq = q(h), 1 x 128 blocks
 //                 out[t] = RN_bf16( sum_s weight[t][s] * (W2[e] . hq) )
 //
-// Bound by reading the weight from HBM (every byte once per launch), for the smallest sizes by latency:
+// Bound by reading the weight from HBM (once per launch; an expert's once per 16 of its pairs, then from L2), for the
+// smallest sizes by latency:
 //  * a ring of stages, each a 128 x 128 weight tile (gate and up: two), a token tile, its scales and a TMEM
 //    buffer: warp 0 streams the weights by TMA, warp 1 issues the MMAs, three to five warps build the
 //    token tiles (FP8 rows come by TMA, the experts' hidden rows are copied, bf16 rows quantized on the
@@ -16,7 +18,7 @@
 //    scales in fp32 registers (a thread owns one weight row).  One commit per stage frees it for the producer
 //    and hands it to the adders.  Rings and commits of their own for weights, tokens and TMEM took the
 //    issuer 1200 to 1600 cycles a unit, more than a unit's bytes take from HBM.
-//  * two CTAs per SM for up to 16 tokens: 100 to 190 KB per SM are in flight;
+//  * two CTAs per SM for up to 16 columns: 100 to 190 KB per SM are in flight;
 //  * the contraction is cut over a cluster of up to 8 CTAs; their fp32 sums meet in distributed shared
 //    memory and are added in range order, so results do not depend on timing and no workspace is needed.
 //  * experts: each CTA sorts the (token, slot) pairs by expert itself (a few hundred ids), so there is no
@@ -25,6 +27,14 @@
 //    expert order.  Launched with programmatic dependence, the second fills its ring with weights while the
 //    first still runs, and waits only before it reads hq.
 //  * every wait is bounded, as in the per-tensor GEMM.
+//
+// Measured (GB/s of 6551): one row of FP8 tokens by 4096 x 1024 4.5 us, by 8192 x 8192 15.6 us (4300), 64 rows by
+// 8192 x 2048 9.0 us; 8 bf16 rows by 1024 x 4096 7.0 us, by 8192 x 8192 18.5 us.  Experts: one token x 2 of 8
+// (1024, 4096) 16 us, 16 x 8 of 64 (2048, 1024) 73 us (4880; the first launch at 5100, the second, 128 CTAs that
+// each hold 80 KB in flight, at 4300), 61 x 4 of 16 (4096, 1360) 76 us, 64 x 8 of 64 95 us.  The smallest are
+// latency: 1 us from the launch to the first copy, 1.3 us to its arrival, 1.5 us from the last block to the
+// output over the cluster.  Tried and dropped: clusters of 16 (at most 14 run at once, where a layer of 2048
+// outputs needs 16), and a whole SM's memory for launches of fewer CTAs than SMs (15 clusters of 8 fit then).
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <cuda_bf16.h>
@@ -57,8 +67,8 @@ constexpr int ctas_per_sm(int nmax) { return nmax == 16 ? 2 : 1; }
 constexpr int smem_budget(int nmax) { return ctas_per_sm(nmax) == 2 ? 112 * 1024 : 224 * 1024; }
 constexpr int tmem_cols(int nmax) { return 512 / ctas_per_sm(nmax); }
 constexpr int builders(int nmax) { return nmax == 16 ? 3 : 5; }
-// Four adders, one per quarter of the weight rows; of 64 columns each of eight takes 32.  (With four, 64 columns'
-// adders took 1050 cycles a unit, twice what its bytes take, mostly to fetch their unrolled code the first time.)
+// Four adders, one per quarter of the weight rows; of 64 columns each of eight takes 32.  (64 rows of 8192 x
+// 2048: 11.3 us with four, 10.6 with eight.)
 constexpr int adders(int nmax) { return nmax == 16 ? 4 : 8; }
 constexpr int threads_of(int nmax) { return 32 * (kFirstBuilder + builders(nmax) + adders(nmax)); }
 // A builder waits for a stage's last use without having seen the uses between.  Units complete in order (one
@@ -1031,6 +1041,7 @@ int launch_stream(const CUtensorMap& map_w, const CUtensorMap& map_x, StreamArgs
                   int64_t units, int64_t grid, cudaStream_t stream) {
     // the sums' exchange lies over the ring
     static_assert(min_stages(NMAX) * stage_bytes(kMode, NMAX) >= tiles_of(kMode) * NMAX * kBM * 4, "exchange");
+    static_assert(kMode >= kUp || stages_for<kMode, NMAX>(0, 0) > 0, "shared memory");
     static_assert(kMode < kUp || min_stages(NMAX) * stage_bytes(kMode, NMAX) >= build_scratch(threads_of(NMAX)), "table");
     static_assert(kMode != kDown || min_stages(NMAX) * stage_bytes(kMode, NMAX) >= FP8DSA_MOE_MAX_TOKENS * kBM * 4, "exchange");
     const cudaError_t se = kernel_setup<kMode, NMAX>();
@@ -1038,7 +1049,7 @@ int launch_stream(const CUtensorMap& map_w, const CUtensorMap& map_x, StreamArgs
     const int split_log = g.splits == 8 ? 3 : g.splits == 4 ? 2 : g.splits - 1;
     const int recv = (kMode == kDown ? g.tokens : is_up(kMode) ? tiles_of(kMode) * own_columns(g, split_log) * g.splits : g.ncols) * kBM * 4;
     // no more stages than a CTA has units; the sums' room apart, where that does not cost a stage (one token
-    // 4.9 -> 4.4 us)
+    // 4.9 -> 4.5 us)
     g.stages = stages_for<kMode, NMAX>(table_size, out_size);
     g.stages = static_cast<int>(std::max<int64_t>(min_stages(NMAX), std::min<int64_t>(g.stages, units)));
     g.off_table = g.stages * (stage_bytes(kMode, NMAX) + 2 * NMAX * 4) + kBarBytes;
