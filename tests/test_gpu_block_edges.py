@@ -174,3 +174,71 @@ def test_product_plain_launches_and_the_profiler(m):
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(out.view(torch.int16), want.view(torch.int16))
+
+
+def test_offsets_past_32_bits():
+    """More than 2^31 elements: the last rows and columns of the quantizers equal those of a small call, and the
+    last columns of a product agree with fp64."""
+    rows, cols = 66048, 33024
+    gen = torch.Generator(device=DEV).manual_seed(1)
+    x = torch.empty(rows, cols, dtype=torch.bfloat16, device=DEV)
+    for r in range(0, rows, 8256):
+        x[r:r + 8256] = torch.randn(8256, cols, device=DEV, generator=gen)
+    rb, cb = rows // 128, cols // 128
+
+    def quantize(x):
+        r, c = x.shape
+        out = [torch.empty(r, c, dtype=torch.uint8, device=DEV) for _ in range(2)]
+        s = [torch.empty(c // 128, r, device=DEV), torch.empty(r // 128, c, device=DEV)]
+        F.fp8_quantize_block(x, F.FP8_IN_BF16, r, c, F.FP8_E4M3, out[0], s[0], out[1], s[1])
+        return out, s
+    (q, qc), (s, sc) = quantize(x)
+    tail = x[-256:, -512:].contiguous()
+    (tq, tqc), (ts, tsc) = quantize(tail)
+    torch.cuda.synchronize()
+    assert torch.equal(q[-256:, -512:], tq) and torch.equal(qc[-256:, -512:], tqc)
+    assert torch.equal(s[-4:, -256:], ts) and torch.equal(sc[-2:, -512:], tsc)
+    del qc, sc
+    w8, ws = torch.empty(rows, cols, dtype=torch.uint8, device=DEV), torch.empty(rb, cb, device=DEV)
+    F.fp8_quantize_block128(x, F.FP8_IN_BF16, rows, cols, F.FP8_E4M3, w8, ws)
+    t8, t_s = torch.empty(256, 512, dtype=torch.uint8, device=DEV), torch.empty(2, 4, device=DEV)
+    F.fp8_quantize_block128(tail, F.FP8_IN_BF16, 256, 512, F.FP8_E4M3, t8, t_s)
+    torch.cuda.synchronize()
+    assert torch.equal(w8[-256:, -512:], t8) and torch.equal(ws[-2:, -4:], t_s)
+    wv = (w8[-16:].view(torch.float8_e4m3fn).double().reshape(16, cb, 128) * ws[-1].double()[None, :, None]).reshape(16, cols)
+    for m in (3, 130):
+        a, sa = q[:m].contiguous(), s[:, :m].contiguous()
+        out = _gemm(a, w8, m, rows, cols, 1, 0, 0, F.BlockScale(sa, 1, 1, m), F.BlockScale(ws, 128, cb, 1))[0]
+        av = (a.view(torch.float8_e4m3fn).double().reshape(m, cb, 128) * sa.T.double()[:, :, None]).reshape(m, cols)
+        ref = (av @ wv.T).cpu().numpy()
+        tol = OB.tolerance(ref, (av.abs() @ wv.abs().T).cpu().numpy(), cols)
+        assert (np.abs(out[:, -16:].double().cpu().numpy() - ref) <= tol).all()
+
+
+def test_experts_past_32_bits():
+    """Weights of more than 2^31 bytes: naming the last four experts gives the bits of a call that has only those."""
+    rng = np.random.default_rng(9)
+    experts, hidden, inter, tokens, topk = 64, 4096, 8192, 2, 2
+    gen = torch.Generator(device=DEV).manual_seed(2)
+
+    def codes(*shape):
+        q = torch.randint(0, 256, shape, dtype=torch.uint8, device=DEV, generator=gen)
+        return torch.where((q & 0x7F) == 0x7F, torch.full_like(q, 0x38), q)
+    w13, w2 = codes(experts, 2 * inter, hidden), codes(experts, hidden, inter)
+    s13, s2 = _scales(rng, experts, 2, inter // 128, hidden // 128) * 2.0 ** -14, _scales(rng, experts, hidden // 128, inter // 128) * 2.0 ** -10
+    x = torch.from_numpy(rng.standard_normal((tokens, hidden)).astype(np.float32)).to(torch.bfloat16).to(DEV)
+    wts = torch.from_numpy(rng.random((tokens, topk)).astype(np.float32)).to(DEV)
+
+    def run(first, ids):
+        e = experts - first
+        nbytes = F.moe_forward_fp8_block_workspace_size(tokens, topk, e, hidden, inter)
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=DEV)
+        out = torch.zeros(tokens, hidden, dtype=torch.bfloat16, device=DEV)
+        F.moe_forward_fp8_block(x, torch.tensor(ids, dtype=torch.int32, device=DEV), wts, tokens, topk, e, hidden, inter, F.FP8_E4M3,
+                                w13[first:], s13[first:], w2[first:], s2[first:], ws, nbytes, out)
+        torch.cuda.synchronize()
+        assert F.fp8_get_device_status() == 0
+        return out
+    far, near = run(0, [[63, 60], [62, 61]]), run(60, [[3, 0], [2, 1]])
+    assert torch.isfinite(far).all() and far.abs().max() > 0
+    assert torch.equal(far, near)
