@@ -29,7 +29,8 @@
 // TFLOP/s; the tensor pipe is 55% busy at 4096^3, 70 us), 8192^3 with a scale per column on both sides 797 us.
 // Tried there and slower: a TMEM load shape that gives a thread four rows and a quarter of the columns, with
 // a quarter of the reads of the scales (4096^3 107 -> 110 us); the next block's first sums loaded before
-// the last ones are added (spills 54 registers: 70 -> 107 us).
+// the last ones are added (spills 54 registers: 70 -> 107 us); barriers, buffers and an issuer for each half of
+// the columns (70 -> 80 us); scalar adds (70 -> 77 us).
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <cuda_bf16.h>

@@ -30,11 +30,11 @@
 //
 // Measured (GB/s of 6551): one row of FP8 tokens by 4096 x 1024 4.5 us, by 8192 x 8192 15.6 us (4300), 64 rows by
 // 8192 x 2048 9.0 us; 8 bf16 rows by 1024 x 4096 7.0 us, by 8192 x 8192 18.5 us.  Experts: one token x 2 of 8
-// (1024, 4096) 16 us, 16 x 8 of 64 (2048, 1024) 73 us (4880; the first launch at 5100, the second, 128 CTAs that
-// each hold 80 KB in flight, at 4300), 61 x 4 of 16 (4096, 1360) 76 us, 64 x 8 of 64 95 us.  The smallest are
+// (1024, 4096) 16 us, 16 x 8 of 64 (2048, 1024) 73 us (4880), 61 x 4 of 16 (4096, 1360) 76 us, 64 x 8 of 64 95 us.  The smallest are
 // latency: 1 us from the launch to the first copy, 1.3 us to its arrival, 1.5 us from the last block to the
-// output over the cluster.  Tried and dropped: clusters of 16 (at most 14 run at once, where a layer of 2048
-// outputs needs 16), and a whole SM's memory for launches of fewer CTAs than SMs (15 clusters of 8 fit then).
+// output over the cluster.  Tried and dropped for the second launch, whose 16 tiles of 2048 outputs give
+// 128 CTAs: clusters of 16 (7 fit at one CTA per SM, so 14 of the 16 needed at two); a whole SM's memory each (15
+// clusters of 8 fit then: 73 -> 95 us); two clusters per tile whose sums meet in global memory (73 -> 74 us).
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <cuda_bf16.h>
