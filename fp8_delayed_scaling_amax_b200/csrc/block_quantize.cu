@@ -12,7 +12,7 @@
 // 16-lane shuffle, a column's one shuffle and an 8-warp shared-memory maximum.  x is read once for
 // both orientations, and the column sums of the tile (the bias gradient's partial sums) come
 // from the same registers.  Bound by HBM: 2 bytes in and 1 out per bf16 element and orientation.
-// Measured, bf16 8192^2 (GB/s of 6551 measured): rows 6290, columns 6300, both 5540, squares 6140.  With
+// Measured, bf16 8192^2 (GB/s of 6551 measured): rows 6290, columns 6300, both 5540, squares 6310.  With
 // the elements unpacked in registers (two CTAs per SM, 128 registers) and bounds checks on every row it
 // was 1870 to 2100; 2048 x 1024 takes 2.6 to 4.4 us, mostly the launch and one HBM round trip.
 #include <cuda_runtime.h>
@@ -305,8 +305,12 @@ __device__ __forceinline__ void quant_tile(const BlockQuantArgs& g, int64_t tr, 
     }
 }
 
+// CTAs per SM.  Squares of 16-bit types fit in 64 registers (8192^2: 32.8 us with three, 31.9 with four); the other modes
+// spill there (2048 x 1024 in both orientations: 4.2 us with three, 4.7 with four).
+constexpr int ctas_per_sm(int in, bool square) { return in == FP8_IN_F32 ? 2 : square ? 4 : 3; }
+
 template <int kIn, int kFmt, bool kRow, bool kCol, bool kSquare>
-__global__ void __launch_bounds__(kThreads, kIn == FP8_IN_F32 ? 2 : 3) block_quant_kernel(const __grid_constant__ BlockQuantArgs g) {
+__global__ void __launch_bounds__(kThreads, ctas_per_sm(kIn, kSquare)) block_quant_kernel(const __grid_constant__ BlockQuantArgs g) {
     __shared__ float red[8][kB];
     __shared__ float inv_col[kB];
     pdl_trigger();
