@@ -61,8 +61,8 @@ constexpr int kMaxSplit = 8;
 enum Mode : int { kDenseFp8 = 0, kDenseBf16 = 1, kUp = 2, kDown = 3, kUpFp8 = 4 };
 constexpr bool is_up(int mode) { return mode == kUp || mode == kUpFp8; }
 
-// Two CTAs per SM (96 registers per thread, 112 KB each) for up to 16 columns; the wide instances hold 64
-// sums per thread, or the outputs of 64 tokens, and take an SM alone.
+// Two CTAs per SM (96 registers per thread, 112 KB each) for up to 16 columns; the instance of 64 columns takes an SM
+// alone (stages of 24 KB and 64 columns of TMEM).
 constexpr int ctas_per_sm(int nmax) { return nmax == 16 ? 2 : 1; }
 constexpr int smem_budget(int nmax) { return ctas_per_sm(nmax) == 2 ? 112 * 1024 : 224 * 1024; }
 constexpr int tmem_cols(int nmax) { return 512 / ctas_per_sm(nmax); }
