@@ -93,6 +93,7 @@ struct Cfg {
     static_assert(kStages >= 4, "too few pipeline stages");
     static_assert(kBM * (BN + kRedPad) * 4 <= kStages * (kAStage + kBStage), "split-K exchange exceeds the stages");
     static_assert((2 * kStages + 2 * kAccBufs + 2) * 8 <= kBarBytes, "barrier area");
+    static_assert(kSmem >= kTmemWholeSmem, "a CTA shares its SM's TMEM with no other");
 };
 
 struct Scales {

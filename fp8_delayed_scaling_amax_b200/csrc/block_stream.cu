@@ -66,6 +66,10 @@ constexpr bool is_up(int mode) { return mode == kUp || mode == kUpFp8; }
 constexpr int ctas_per_sm(int nmax) { return nmax == 16 ? 2 : 1; }
 constexpr int smem_budget(int nmax) { return ctas_per_sm(nmax) == 2 ? 112 * 1024 : 224 * 1024; }
 constexpr int tmem_cols(int nmax) { return 512 / ctas_per_sm(nmax); }
+// A short product's ring is small: a launch takes this much shared memory all the same, so that no more CTAs share
+// an SM than its TMEM serves.
+constexpr int smem_least(int nmax) { return tmem_cols(nmax) <= 256 ? kTmemHalfSmem : kTmemWholeSmem; }
+static_assert(smem_least(16) <= smem_budget(16) && smem_least(64) <= smem_budget(64), "shared memory");
 constexpr int builders(int nmax) { return nmax == 16 ? 3 : 5; }
 // Four adders, one per quarter of the weight rows; of 64 columns each of eight takes 32.  (64 rows of 8192 x
 // 2048: 11.3 us with four, 10.6 with eight.)
@@ -1060,6 +1064,7 @@ int launch_stream(const CUtensorMap& map_w, const CUtensorMap& map_x, StreamArgs
         g.off_recv = static_cast<int>(bytes);
         bytes += static_cast<size_t>(recv);
     }
+    bytes = std::max(bytes, static_cast<size_t>(smem_least(NMAX)));
     const int rc = wait_ctl(&g.wait);
     if (rc) return rc;
     const cudaError_t e = launch_ex(block_stream_kernel<kMode, NMAX>, dim3(static_cast<unsigned>(grid)), dim3(threads_of(NMAX)),

@@ -103,6 +103,7 @@ struct Cfg {
     static constexpr int kSmem = kFixed + kStages * (kAStage + kBStage);
     static constexpr uint32_t kTxBytes = (kPair ? 2u : 1u) * (kAStage + kBStage);
     static_assert(kStages >= 3, "too few pipeline stages");
+    static_assert(kSmem >= kTmemWholeSmem, "a CTA shares its SM's TMEM with no other");
 };
 
 // One GEMM of a launch (a launch may carry two, e.g. dX and dW, over one tile space).

@@ -88,6 +88,17 @@ cudaError_t launch_ex(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t sm
     return cudaLaunchKernelEx(&cfg, kernel, static_cast<KArgs>(args)...);
 }
 
+// Tensor memory is 512 columns per SM.  tcgen05.alloc waits, without a limit, for columns that another CTA of
+// the SM holds; where both belong to clusters whose CTAs wait for one another, neither kernel might ever end.  So
+// CTAs that can share an SM never want more than 512 columns together, whatever kernels and streams they come
+// from, and shared memory sees to it (register counts would today, but nothing keeps them): a CTA with up
+// to 256 columns takes at least kTmemHalfSmem bytes of it, so that no three fit, any other at least
+// kTmemWholeSmem, beside which none of the others fits.
+constexpr int kTmemHalfSmem = 77 * 1024, kTmemWholeSmem = 150 * 1024;
+constexpr int kSmemPerSm = 228 * 1024, kSmemReserved = 1024;  // sm_100; the system's share of every CTA
+static_assert(3 * (kTmemHalfSmem + kSmemReserved) > kSmemPerSm, "three CTAs of 256 columns");
+static_assert(kTmemHalfSmem + kTmemWholeSmem + 2 * kSmemReserved > kSmemPerSm, "256 and 512 columns");
+
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 inline size_t align_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
