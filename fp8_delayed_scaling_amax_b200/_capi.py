@@ -394,6 +394,7 @@ def fp8_gemm_block(a, b, fmt_a, fmt_b, layout, m, n, k, lda, ldb, ldo, batch, st
 
 
 def linear_forward_fp8_block_workspace_size(m, k, n) -> int:
+    """Workspace bytes; with n = 0 what a forward with an fp8 weight (or w8_out) uses."""
     return int(lib().linear_forward_fp8_block_workspace_size(int(m), int(k), int(n)))
 
 

@@ -45,6 +45,18 @@ FwdLayout fwd_layout(int64_t m, int64_t k, int64_t n) {
     return L;
 }
 
+// Whether the product quantizes x itself (at most kStreamMaxBf16Rows rows, whose column form nobody wants): one launch, no x8.
+bool quantizes_inside(int64_t m, int64_t k, int64_t n, const uint8_t* x8c_out) {
+    return m > 0 && k > 0 && n > 0 && x8c_out == nullptr && m <= kStreamMaxBf16Rows;
+}
+
+// What a call touches of its layout: all of it where w is quantized into the workspace, x8 with its scales (which
+// lie first) where only x is, nothing where the product quantizes x.
+size_t fwd_need(int64_t m, int64_t k, int64_t n, bool w8_elsewhere, const uint8_t* x8c_out) {
+    const FwdLayout L = fwd_layout(m, k, n);
+    return !w8_elsewhere ? L.total : quantizes_inside(m, k, n, x8c_out) ? 0 : L.w8;
+}
+
 struct BwdLayout {
     size_t g8, sg, g8c, sgc, colsum, total;
 };
@@ -105,7 +117,8 @@ extern "C" int linear_forward_fp8_block(const void* x, const void* w, int w_is_f
                                         size_t workspace_bytes, void* y, cudaStream_t stream) {
     clear_error();
     if (!valid_fmt(fmt)) return fail(FP8DSA_ERR_INVALID_ARG, "fmt must be FP8_E4M3 or FP8_E5M2");
-    int rc = check_common(m, k, n, workspace, workspace_bytes, linear_forward_fp8_block_workspace_size(m, k, n));
+    int rc = check_common(m, k, n, workspace, workspace_bytes,
+                          sizes_ok(m, k, n) ? fwd_need(m, k, n, w_is_fp8 || w8_out != nullptr, x8c_out) : 0);
     if (rc) return rc;
     const bool has_x = m > 0 && k > 0, has_w = n > 0 && k > 0, has_y = m > 0 && n > 0;
     if ((has_x && x == nullptr) || (has_w && w == nullptr) || (has_y && y == nullptr))
@@ -141,7 +154,7 @@ extern "C" int linear_forward_fp8_block(const void* x, const void* w, int w_is_f
         sw = j.scale_row;
     }
     const fp8_block_scale_t sb{sw, 128, blocks_of(k), 1, 0};
-    if (has_x && has_y && x8c_out == nullptr && m <= kStreamMaxBf16Rows) {
+    if (quantizes_inside(m, k, n, x8c_out)) {
         const BlockGemmDesc d = product(static_cast<const uint8_t*>(x), w8, fmt, fmt, 0, 0, m, n, k, {}, sb, bias, y);
         return block_stream_gemm(d, true, stream);
     }

@@ -453,7 +453,8 @@ int fp8_gemm_block(const uint8_t* a, const uint8_t* b, fp8_fmt_t fmt_a, fp8_fmt_
                    const fp8_block_scale_t* scale_a, const fp8_block_scale_t* scale_b,
                    const void* bias, void* out, cudaStream_t stream);
 
-/* Workspace bytes of linear_forward_fp8_block: x8 and w8 with their scales. */
+/* Workspace bytes of linear_forward_fp8_block: x8 and w8 with their scales.  With n = 0: x8 with its scales
+ * alone, which is all that a call with an fp8 w, or with w8_out, uses. */
 size_t linear_forward_fp8_block_workspace_size(int64_t m, int64_t k, int64_t n);
 
 /* Linear layer y = x w^T + bias with block scaling (the block-scaled counterpart of linear_forward_fp8):
@@ -465,7 +466,8 @@ size_t linear_forward_fp8_block_workspace_size(int64_t m, int64_t k, int64_t n);
  *   weight, x8c_out [m][k] and x8c_scale_out [ceil(m/128)][k] (both or neither) x in 128 x 1 blocks down
  *   the tokens, in `fmt`; byte tensors 16-byte aligned.
  *   workspace: dev, >= linear_forward_fp8_block_workspace_size(m, k, n) bytes, 256-byte aligned, no
- *   initial contents.  k and n must be multiples of 16.
+ *   initial contents; with an fp8 w or w8_out ...(m, k, 0) bytes are enough, and with at most 16 rows of x and
+ *   no x8c_out besides none are used (NULL and 0).  k and n must be multiples of 16.
  *   An fp8 weight with at most 16 rows of x and no x8c_out (decoding) is one launch. */
 int linear_forward_fp8_block(const void* x, const void* w, int w_is_fp8, const float* w_scale, const void* bias,
                              int64_t m, int64_t k, int64_t n, fp8_fmt_t fmt, uint8_t* w8_out,
