@@ -208,28 +208,24 @@ __device__ __forceinline__ void build_table(const Table& t, const StreamArgs& g,
         if (kWeights) t.weight[pos] = w;
     };
     if (g.pairs <= 32) {
-        // one warp, in registers; entries in the order of their first pair
+        // one warp, in registers: a pair's position is the number of pairs with a smaller expert, found bit by bit, and
+        // of those before it with the same one
         if (tid < 32) {
             const int e0 = first.id;
             const bool valid = e0 >= 0 && e0 < g.experts;
-            const uint32_t mask = __match_any_sync(0xFFFFFFFFu, valid ? e0 : -1);
-            const uint32_t below = (1u << lane) - 1u;
-            const int rank = __popc(mask & below);
+            uint32_t less = 0u, same = __ballot_sync(0xFFFFFFFFu, valid);
+#pragma unroll 1
+            for (int bit = 31 - __clz(g.experts - 1); bit >= 0; --bit) {
+                const bool one = (e0 >> bit & 1) != 0;
+                const uint32_t ones = __ballot_sync(0xFFFFFFFFu, one);
+                if (one) less |= same & ~ones;
+                same &= one ? ones : ~ones;
+            }
+            const int rank = __popc(same & ((1u << lane) - 1u)), pos = __popc(less) + rank;
             const bool leader = valid && rank % kRun == 0;  // the first pair of an entry
             const uint32_t leaders = __ballot_sync(0xFFFFFFFFu, leader);
-            const int n = leader ? min(kRun, __popc(mask) - rank) : 0;
-            int start = n;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int v = __shfl_up_sync(0xFFFFFFFFu, start, o);
-                if (lane >= o) start += v;
-            }
-            start -= n;
-            if (leader) t.entries[__popc(leaders & below)] = pack_entry(e0, start, n);
-            // this pair's entry starts at the last leader of its expert up to itself
-            const uint32_t mine = leaders & mask & (below | (1u << lane));
-            const int from = __shfl_sync(0xFFFFFFFFu, start, valid ? 31 - __clz(mine) : lane);
-            if (valid) place(from + rank % kRun, lane, first.weight);
+            if (leader) t.entries[__popc(leaders & less) + rank / kRun] = pack_entry(e0, pos, min(kRun, __popc(same) - rank));
+            if (valid) place(pos, lane, first.weight);
             if (lane == 0) *t.total = __popc(leaders);
         }
         __syncthreads();

@@ -507,14 +507,15 @@ size_t moe_forward_fp8_block_workspace_size(int64_t tokens, int64_t topk, int64_
  *       (g, u) = q(x[t]) . w13[e]^T         q: fp8_quantize_block, 1 x 128 blocks, in fmt
  *       h      = q( g / (1 + exp(-g)) * u ) formed and quantized from fp32
  *   out[t] = RN_bf16( sum_s weights[t][s] * (h . w2[e]^T) )
- * with the block scales applied and every sum in fp32; deterministic.
+ * with the block scales applied and every sum in fp32; deterministic.  A token's experts are added in the experts'
+ * order: which slot names which expert does not show in the output (slots that name the same one keep their order).
  *   x: dev bf16 [tokens][hidden]; ids: dev int32 [tokens][topk]; weights: dev fp32 [tokens][topk].
  *   w13: dev bytes in fmt [experts][2 inter][hidden], the gate's rows before the up rows, 16-byte aligned;
  *   w13_scale: dev fp32 [experts][2][ceil(inter/128)][ceil(hidden/128)] (gate and up each have 128 x 128
  *   blocks of their own: fp8_quantize_block128 of each [inter][hidden] half);
  *   w2: dev bytes in fmt [experts][hidden][inter], 16-byte aligned;
  *   w2_scale: dev fp32 [experts][ceil(hidden/128)][ceil(inter/128)].
- *   tokens <= 64, topk <= 32, experts <= 1024; hidden and inter multiples of 16.
+ *   tokens <= 64, topk <= 32, experts <= 1024; hidden and inter multiples of 16 up to 2^24.
  *   workspace: dev, >= moe_forward_fp8_block_workspace_size(...) bytes, 256-byte aligned, no initial
  *   contents; calls that may overlap need one each.  out: dev bf16 [tokens][hidden].
  * Only the weights of experts that are named are read.  Not on the pages. */
