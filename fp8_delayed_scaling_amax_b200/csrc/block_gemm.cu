@@ -24,9 +24,10 @@
 //    scales of the current block in shared memory and reads them back as broadcasts.
 //  * every wait is bounded, as in the per-tensor GEMM.
 //
-// Bound by the promotion: a 256 x 256 pair block takes 950 cycles with one scale per thread and 1500 with
-// a scale per column (a multiply more for each sum), its MMAs 512.  Measured: 8192^3 537 to 557 us (2000
-// TFLOP/s; the tensor pipe is 55% busy at 4096^3, 70 us), 8192^3 with a scale per column on both sides 797 us.
+// Bound by the promotion: a 256 x 256 pair block takes 0.48 us with one scale per thread and 0.73 with a
+// scale per column (a multiply more for each sum; the slopes of 2048 x 2048 over K = 4096 and 8192), its MMAs 0.26
+// (512 cycles).  Measured: 8192^3 470 to 563 us by the inputs' power (2000 TFLOP/s; the tensor pipe is 55% busy at
+// 4096^3, 67 to 70 us), 8192^3 with a scale per column on both sides 797 to 816 us.
 // Tried there and slower: a TMEM load shape that gives a thread four rows and a quarter of the columns, with
 // a quarter of the reads of the scales (4096^3 107 -> 110 us); the next block's first sums loaded before
 // the last ones are added (spills 54 registers: 70 -> 107 us); barriers, buffers and an issuer for each half of
@@ -54,8 +55,10 @@ constexpr int kEpiThreads = 32 * kEpiWarps;
 // Promotion of a 256-wide tile needs more than the 168 registers that eleven warps leave a thread
 // (128 sums and 64 values in flight): its warps are two whole warpgroups that take over registers of
 // the first one (warp 3 only fills that).  384 threads launch with 168 each, 64,512 in all;
-// 128 x 56 + 256 x 224 = 64,512.  Nothing may spill: with all but 28 KB of an SM's L1 used as
-// shared memory, spilled registers go to L2 (8192^3 with 136 bytes of spills: 1357 against 1850 TFLOP/s).
+// 128 x 56 + 256 x 224 = 64,512.  Spills are dear: with all but 28 KB of an SM's L1 used as
+// shared memory, they go to L2 (8192^3 with 136 bytes of spills: 1357 against 1850 TFLOP/s).  ptxas reports none but for
+// the 256-wide instance with a scale per column, which stores 24 bytes and loads 48 (gone without the bias's code,
+// which a tile runs once; larger shares of the registers do not change them).
 template <bool kRegSplit>
 struct Roles {
     static constexpr int kFirstEpiWarp = kRegSplit ? 4 : 1 + kIssuers;
@@ -256,7 +259,7 @@ __global__ void __launch_bounds__(Roles<kPair>::kThreads, 1)
         } else if (warp <= kIssuers) {
             // ------------------------------------------------------------------ MMA issuers (leader)
             // Two threads take the K blocks in turn, each with half of the TMEM buffers: one block's waits
-            // and commits (520 of about 970 cycles with a single issuer) run beside the other's MMAs.
+            // and commits run beside the other's MMAs.
             if (leader && lane == 0) {
                 const int first = warp - 1;
                 const int64_t my_tiles = (g.num_tiles - 1 - unit) / units + 1;
@@ -463,9 +466,9 @@ __global__ void __launch_bounds__(Roles<kPair>::kThreads, 1)
 
             if constexpr (!kSplit) {
                 // ---------------------------------------------------------- output of the whole tile
-                // Compact code: it runs once per tile, and instruction fetches are most of its time (with the
-                // bias and the direct stores inside the unrolled loop 3700 cycles a tile; moving them out
-                // took 2048 x 4096 x 1024 from 17.6 to 15.0 us).
+                // Compact code: it runs once per tile, and instruction fetches are most of its time (moving the
+                // bias and the direct stores out of the unrolled loop took 2048 x 4096 x 1024 from 17.6 to
+                // 15.0 us).
                 if (lane == 0) bulk_wait_group_read<0>();  // the last tile's stores have read the boxes
                 __syncwarp();
                 if (g.bias != nullptr) {

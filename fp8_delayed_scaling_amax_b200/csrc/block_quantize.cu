@@ -12,7 +12,8 @@
 // 16-lane shuffle, a column's one shuffle and an 8-warp shared-memory maximum.  x is read once for
 // both orientations, and the column sums of the tile (the bias gradient's partial sums) come
 // from the same registers.  Bound by HBM: 2 bytes in and 1 out per bf16 element and orientation.
-// Measured, bf16 8192^2 (GB/s of 6551 measured): rows 6290, columns 6300, both 5540, squares 6310.  With
+// Measured, 8192^2 (GB/s of 6551 measured): bf16 rows 6290, columns 6300, both 5540, squares 6420; fp32 rows 6060 to 6560,
+// both 5770 to 6230, squares 6660.  With
 // the elements unpacked in registers (two CTAs per SM, 128 registers) and bounds checks on every row it
 // was 1870 to 2100; 2048 x 1024 takes 2.6 to 4.4 us, mostly the launch and one HBM round trip.
 #include <cuda_runtime.h>
@@ -306,7 +307,9 @@ __device__ __forceinline__ void quant_tile(const BlockQuantArgs& g, int64_t tr, 
 }
 
 // CTAs per SM.  Squares of 16-bit types fit in 64 registers (8192^2: 32.8 us with three, 31.9 with four); the other modes
-// spill there (2048 x 1024 in both orientations: 4.2 us with three, 4.7 with four).
+// spill there (2048 x 1024 in both orientations: 4.2 us with three, 4.7 with four).  With three, 80 registers, both
+// orientations of 16-bit types spill 16 bytes a thread, the other modes nothing; fp32, whose elements take 64 registers,
+// has two.
 constexpr int ctas_per_sm(int in, bool square) { return in == FP8_IN_F32 ? 2 : square ? 4 : 3; }
 
 template <int kIn, int kFmt, bool kRow, bool kCol, bool kSquare>

@@ -16,8 +16,8 @@
 //    token tiles (FP8 rows come by TMA, the experts' hidden rows are copied, bf16 rows quantized on the
 //    way: 1 x 128 blocks never leave a tile) and fetch the scales, four or eight add the blocks with their
 //    scales in fp32 registers (a thread owns one weight row).  One commit per stage frees it for the producer
-//    and hands it to the adders.  Rings and commits of their own for weights, tokens and TMEM took the
-//    issuer 1200 to 1600 cycles a unit, more than a unit's bytes take from HBM.
+//    and hands it to the adders.  (With rings and commits of their own for weights, tokens and TMEM the issuer took
+//    longer over a unit than the unit's bytes take from HBM.)
 //  * two CTAs per SM for up to 16 columns: 100 to 190 KB per SM are in flight;
 //  * the contraction is cut over a cluster of up to 8 CTAs; their fp32 sums meet in distributed shared
 //    memory and are added in range order, so results do not depend on timing and no workspace is needed.
@@ -28,11 +28,11 @@
 //    first still runs, and waits only before it reads hq.
 //  * every wait is bounded, as in the per-tensor GEMM.
 //
-// Measured (GB/s of 6551): one row of FP8 tokens by 4096 x 1024 4.5 us, by 8192 x 8192 15.6 us (4300), 64 rows by
-// 8192 x 2048 9.0 us; 8 bf16 rows by 1024 x 4096 7.0 us, by 8192 x 8192 18.5 us.  Experts: one token x 2 of 8
-// (1024, 4096) 16 us, 16 x 8 of 64 (2048, 1024) 73 us (4880), 61 x 4 of 16 (4096, 1360) 76 us, 64 x 8 of 64 95 us.  The smallest are
-// latency: 1 us from the launch to the first copy, 1.3 us to its arrival, 1.5 us from the last block to the
-// output over the cluster.  Tried and dropped for the second launch, whose 16 tiles of 2048 outputs give
+// Measured (GB/s of 6551), weights from HBM: one row of FP8 tokens by 4096 x 1024 5.2 us (4.5 from L2), by 8192 x 8192
+// 14.6 us (4600), 64 rows by 8192 x 2048 8.7 us, by 8192 x 8192 16.9; 8 bf16 rows by 1024 x 4096 7.2 us, by 8192 x 8192
+// 18.5 us.  Experts: one token x 2 of 8 (1024, 4096) 15.3 us, 16 x 8 of 64 (2048, 1024) 70 us (5070), 61 x 4 of 16
+// (4096, 1360) 76 us, 64 x 8 of 64 95 us.  The smallest are latency: 1 us from the launch to the first copy, 1.3 us to its
+// arrival, 1.5 us from the last block to the output over the cluster.  Tried and dropped for the second launch, whose 16 tiles of 2048 outputs give
 // 128 CTAs: clusters of 16 (7 fit at one CTA per SM, so 14 of the 16 needed at two); a whole SM's memory each (15
 // clusters of 8 fit then: 73 -> 95 us); two clusters per tile whose sums meet in global memory (73 -> 74 us).
 #include <cuda.h>
@@ -176,8 +176,8 @@ __device__ __forceinline__ int token_of(const StreamArgs& g, int pair) {
     return static_cast<int>((static_cast<uint32_t>(pair) * g.topk_inv) >> 16);
 }
 
-// The pairs are dealt to the warps in runs; a thread's first one, loaded before the table is built (a load takes 3000
-// cycles while the first launch streams its weights).
+// The pairs are dealt to the warps in runs; a thread's first one, loaded before the table is built (a load waits
+// long while the first launch streams its weights).
 struct FirstPair {
     int id;
     float weight;
@@ -233,8 +233,8 @@ __device__ __forceinline__ void build_table(const Table& t, const StreamArgs& g,
     }
     // Every warp ranks a run of consecutive pairs within itself and counts them by expert in a row of its own;
     // then a thread per expert sums the rows, and one warp the experts.
-    // One warp ranking all pairs took 6500 cycles for 128 of them; counting, for each pair, the pairs before
-    // it took 20000 for 512.
+    // (One warp ranking all pairs, and counting, for each pair, the pairs before it, took microseconds for a few
+    // hundred of them.)
     constexpr int kWarps = kThreads / 32;
     const int warp = tid >> 5, run = pairs_per_warp(g, kWarps);
     const int rows = (g.pairs + run - 1) / run, e4 = (g.experts + 3) / 4 * 4;
@@ -463,7 +463,7 @@ __global__ void __launch_bounds__(threads_of(NMAX), ctas_per_sm(NMAX))
     FirstPair mine{-1, 0.0f};
     if constexpr (kMode == kDown) mine = load_first<true, kThreads>(g);
     if (warp == 0) {
-        if (lane < R) {  // (thread 0 for all of them took 600 cycles)
+        if (lane < R) {  // (a lane each: one after the other they are on every launch's path)
             mbar_init(full + lane, 2 + kAdders);  // the weights, the tokens, and the adders of the unit a ring ago
             mbar_init(done + lane, 2);  // the MMAs' commit, and the builder (whose scales the adders read)
             fence_mbar_init();
@@ -646,7 +646,7 @@ __global__ void __launch_bounds__(threads_of(NMAX), ctas_per_sm(NMAX))
         auto load = [&](Cursor c, int n, int j0, Batch& out, float (&scale)[kScales], float& w_scale) {
             if (j0 == 0 && lane < kTiles) {
                 // the weight tile's scale (128 x 128 blocks), with the tokens': it may come from HBM, and the
-                // adders, a block ahead at most, waited for it (1300 of 2300 cycles a unit)
+                // adders, a block ahead at most, would wait for it
                 if constexpr (kMoe)
                     w_scale = __ldg(g.w_scale + ((static_cast<int64_t>(entry_at(c.ent).expert) * kTiles + lane) * g.row_tiles +
                                                  tile_of(c.ent)) * g.k_blocks + c.kb);
@@ -764,9 +764,9 @@ __global__ void __launch_bounds__(threads_of(NMAX), ctas_per_sm(NMAX))
         cluster_wait();
     } else {
         // ------------------------------------------------------------------ blocks added with their scales
-        // Two sums at a time: two units of one weight tile each, or a unit's gate and up.  A round is mostly latency
-        // (1500 cycles with a wait per unit, the scales read after the sums and a cursor moved unit by unit),
-        // so the two barriers are looked at together and the scales are multiplied while TMEM is read.  Loops over
+        // Two sums at a time: two units of one weight tile each, or a unit's gate and up.  A round is mostly latency, so the
+        // two barriers are looked at together and the scales are multiplied while TMEM is read (with a wait per unit, the
+        // scales after the sums and scalar adds the experts' 16 tokens x 8 of 64 took 83 us instead of 73).  Loops over
         // columns outside the K loop are rolled: little code, little of it fetched.
         constexpr int kAtOnce = kTiles == 1 ? 2 : 1;
         const int q = warp & 3;
@@ -899,8 +899,7 @@ __global__ void __launch_bounds__(threads_of(NMAX), ctas_per_sm(NMAX))
                     float* most = reinterpret_cast<float*>(smem + g.off_out) + (ent & 1) * 4 * NMAX;  // [warp][column]
                     const int tile = tile_of(ent), at = tile * kBM + row;
                     // Rolled loops that pick a column's registers by comparison: this code runs once per item, and
-                    // unrolled it took 25000 cycles the first time, nearly all of them instruction fetches from
-                    // a memory system that is busy with weights.
+                    // unrolled it would first have to be fetched from a memory system that is busy with weights.
 #pragma unroll 1
                     for (int j = 0; j < n; ++j) {
                         const float h = at < g.inter ? gated(column(acc2[0], j), column(acc2[1], j)) : 0.0f;
