@@ -99,12 +99,6 @@ struct Cfg {
     static_assert(kSmem >= kTmemWholeSmem, "a CTA shares its SM's TMEM with no other");
 };
 
-struct Scales {
-    const float* p;
-    int64_t s_mn, s_kb, s_b;
-    int shift;  // log2(rows per scale): 0 or 7
-};
-
 struct BlockGemmArgs {
     int m, n, k_blocks;
     int tiles_m, tiles_n, num_tiles;
@@ -115,7 +109,7 @@ struct BlockGemmArgs {
     int64_t ldo, stride_o;
     int vec_out, tma_out;
     const uint16_t* bias;
-    Scales sa, sb;
+    BlockScales sa, sb;
     WaitCtl wait;
 };
 
@@ -691,10 +685,6 @@ Plan choose_plan(const BlockGemmDesc& d, int64_t k_blocks, bool col) {
         }
     }
     return best;
-}
-
-Scales scales_of(const fp8_block_scale_t& s) {
-    return Scales{s.scale, s.stride_mn, s.stride_kb, s.stride_batch, s.block_mn == 128 ? 7 : 0};
 }
 
 }  // namespace

@@ -46,11 +46,6 @@ struct BlockQuantArgs {
     int vec_all;           // all of these
 };
 
-__device__ __forceinline__ void block_step(float amax, float fp8_max, float& s, float& inv) {
-    s = fmaxf(__fdiv_rn(amax, fp8_max), 1e-12f);
-    inv = __frcp_rn(s);
-}
-
 // Eight consecutive elements as they are stored: 16-bit types stay packed (4 registers), so a thread's 64
 // elements leave room for three CTAs per SM.
 template <int kIn>
@@ -159,7 +154,6 @@ __device__ __forceinline__ void store8(uint8_t* p, const BlockQuantArgs& g, int 
 template <int kIn, int kFmt, bool kRow, bool kCol, bool kSquare, bool kFull>
 __device__ __forceinline__ void quant_tile(const BlockQuantArgs& g, int64_t tr, int64_t tc, float (&red)[8][kB],
                                            float (&inv_col)[kB]) {
-    constexpr float kMax = kFmt == 0 ? 448.0f : 57344.0f;
     const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int64_t row0 = tr * kB + ty, col0 = tc * kB + tx * kColsPer;
@@ -185,8 +179,7 @@ __device__ __forceinline__ void quant_tile(const BlockQuantArgs& g, int64_t tr, 
         am = red[0][0];
 #pragma unroll
         for (int w = 1; w < 8; ++w) am = fmaxf(am, red[0][w]);
-        float s, inv;
-        block_step(am, kMax, s, inv);
+        const float s = block_step(am, kFmt), inv = __frcp_rn(s);
         if (threadIdx.x == 0) g.scale_row[tr * g.tiles_c + tc] = s;
 #pragma unroll
         for (int r = 0; r < kRowsPer; ++r) {
@@ -213,8 +206,7 @@ __device__ __forceinline__ void quant_tile(const BlockQuantArgs& g, int64_t tr, 
             am = fmaxf(am, hi);
 #pragma unroll
             for (int o = 8; o > 0; o >>= 1) am = fmaxf(am, __shfl_xor_sync(0xFFFFFFFFu, am, o));
-            float s, inv;
-            block_step(am, kMax, s, inv);
+            const float s = block_step(am, kFmt), inv = __frcp_rn(s);
             if (tx == r) mine = s;
             float f[kColsPer];
             v[r].unpack(f);
@@ -254,8 +246,7 @@ __device__ __forceinline__ void quant_tile(const BlockQuantArgs& g, int64_t tr, 
             float a = red[0][c];
 #pragma unroll
             for (int w = 1; w < 8; ++w) a = fmaxf(a, red[w][c]);
-            float s, inv;
-            block_step(a, kMax, s, inv);
+            const float s = block_step(a, kFmt), inv = __frcp_rn(s);
             inv_col[c] = inv;
             const int64_t col = tc * kB + c;
             if (col < g.cols) g.scale_col[tr * g.cols + col] = s;

@@ -85,12 +85,6 @@ constexpr int max_stages(int mode, int nmax) {
     return tmem_cols(nmax) / (tiles_of(mode) * nmax) < kMaxStages ? tmem_cols(nmax) / (tiles_of(mode) * nmax) : kMaxStages;
 }
 
-struct Scales {
-    const float* p;
-    int64_t s_mn, s_kb, s_b;
-    int shift;
-};
-
 struct StreamArgs {
     int splits;       // CTAs per cluster
     int stages;       // ring
@@ -105,7 +99,7 @@ struct StreamArgs {
     int64_t ldx, x_batch;       // elements
     int x_vec;                  // rows are 16-byte aligned
     int w_mn, w_batched, x_batched;
-    Scales sw, sx;
+    BlockScales sw, sx;
     const uint16_t* bias;
     uint16_t* out;
     int64_t ldo, stride_o;
@@ -306,10 +300,6 @@ __device__ __forceinline__ void build_table(const Table& t, const StreamArgs& g,
     }
     fence_proxy_async_smem();  // the ring is TMA's from here on
     __syncthreads();
-}
-
-__device__ __forceinline__ float block_step(float amax, int fmt) {
-    return fmaxf(__fdiv_rn(amax, fmt == 0 ? 448.0f : 57344.0f), 1e-12f);
 }
 
 // One K block of 2 * kPairs bf16 rows, 16 lanes per row (lane l16 holds elements 8 l16 .. of rows 2 r + lane / 16,
@@ -1073,10 +1063,6 @@ int split_for(int64_t tiles, int64_t k_blocks, int ctas) {
     int s = 1;
     while (s < kMaxSplit && 2 * s * tiles <= ctas * sm_count() && k_blocks >= 4 * s) s *= 2;
     return s;
-}
-
-Scales scales_of(const fp8_block_scale_t& s) {
-    return Scales{s.scale, s.stride_mn, s.stride_kb, s.stride_batch, s.block_mn == 128 ? 7 : 0};
 }
 
 }  // namespace

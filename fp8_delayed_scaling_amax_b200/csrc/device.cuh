@@ -517,6 +517,11 @@ __device__ __forceinline__ void ring_fold_deferred(float* st, int n, int idx, fl
     st[n + 2] = 0.0f;
 }
 
+// The scale of a block of 128 (or of 128 x 128) whose largest magnitude is `amax`; fmt 0: E4M3, 1: E5M2.
+__device__ __forceinline__ float block_step(float amax, int fmt) {
+    return fmaxf(__fdiv_rn(amax, fmt == 0 ? 448.0f : 57344.0f), 1e-12f);
+}
+
 __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
     const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
     return *reinterpret_cast<const uint32_t*>(&v);

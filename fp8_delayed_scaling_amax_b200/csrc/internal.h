@@ -190,6 +190,15 @@ struct BlockGemmDesc {
     const void* bias;  // bf16 [n] or null
     void* out;         // bf16
 };
+// An operand's scales as the kernels take them.
+struct BlockScales {
+    const float* p;
+    int64_t s_mn, s_kb, s_b;
+    int shift;  // log2(rows per scale): 0 or 7
+};
+inline BlockScales scales_of(const fp8_block_scale_t& s) {
+    return BlockScales{s.scale, s.stride_mn, s.stride_kb, s.stride_batch, s.block_mn == 128 ? 7 : 0};
+}
 int block_gemm_launch(const BlockGemmDesc& d, cudaStream_t stream);
 // The same for a K-major A of few rows (block_stream.cu): up to kStreamMaxRows FP8 rows, or with x_is_bf16 up to
 // kStreamMaxBf16Rows bf16 rows (strides in elements, sa unused), quantized to fmt_a in 1 x 128 blocks on
