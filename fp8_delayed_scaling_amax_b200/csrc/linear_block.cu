@@ -45,16 +45,17 @@ FwdLayout fwd_layout(int64_t m, int64_t k, int64_t n) {
     return L;
 }
 
-// Whether the product quantizes x itself (at most kStreamMaxBf16Rows rows, whose column form nobody wants): one launch, no x8.
-bool quantizes_inside(int64_t m, int64_t k, int64_t n, const uint8_t* x8c_out) {
-    return m > 0 && k > 0 && n > 0 && x8c_out == nullptr && m <= kStreamMaxBf16Rows;
+// Whether x is quantized by a launch of its own: for its column form, or for a product of more than
+// kStreamMaxBf16Rows rows (with fewer the product quantizes x itself: one launch).
+bool quantizes_x(int64_t m, int64_t k, int64_t n, const uint8_t* x8c_out) {
+    return m > 0 && k > 0 && (x8c_out != nullptr || (n > 0 && m > kStreamMaxBf16Rows));
 }
 
 // What a call touches of its layout: all of it where w is quantized into the workspace, x8 with its scales (which
-// lie first) where only x is, nothing where the product quantizes x.
+// lie first) where only x is.
 size_t fwd_need(int64_t m, int64_t k, int64_t n, bool w8_elsewhere, const uint8_t* x8c_out) {
     const FwdLayout L = fwd_layout(m, k, n);
-    return !w8_elsewhere ? L.total : quantizes_inside(m, k, n, x8c_out) ? 0 : L.w8;
+    return !w8_elsewhere && n > 0 ? L.total : quantizes_x(m, k, n, x8c_out) ? L.w8 : 0;
 }
 
 struct BwdLayout {
@@ -154,13 +155,14 @@ extern "C" int linear_forward_fp8_block(const void* x, const void* w, int w_is_f
         sw = j.scale_row;
     }
     const fp8_block_scale_t sb{sw, 128, blocks_of(k), 1, 0};
-    if (quantizes_inside(m, k, n, x8c_out)) {
+    const bool with_x8 = quantizes_x(m, k, n, x8c_out);
+    if (has_x && has_y && !with_x8) {
         const BlockGemmDesc d = product(static_cast<const uint8_t*>(x), w8, fmt, fmt, 0, 0, m, n, k, {}, sb, bias, y);
         return block_stream_gemm(d, true, stream);
     }
     uint8_t* x8 = ws + L.x8;
     float* sx = reinterpret_cast<float*>(ws + L.sx);
-    if (has_x) {
+    if (with_x8) {
         BlockQuantJob j;
         j.x = x;
         j.rows = m;

@@ -50,6 +50,16 @@ def test_a_weight_kept_elsewhere_takes_no_workspace(m, fp8, w8_out):
     assert rc == INVALID and why.startswith("workspace")
 
 
+@pytest.mark.parametrize("m", [1, 17, 300])
+@pytest.mark.parametrize("fp8", [False, True])
+def test_no_columns_of_the_weight_need_no_workspace(m, fp8):
+    """Without outputs there is nothing to do, unless x's column form is wanted."""
+    rc, why = _forward(m, 1040, 0, fp8)
+    assert rc == INVALID and why.startswith("x, w and y")
+    rc, why = _forward(m, 1040, 0, fp8, x8c_out=True)
+    assert rc == INVALID and why.startswith("workspace")
+
+
 @pytest.mark.parametrize("m", [1, 16, 17, 300])
 def test_a_weight_quantized_in_the_call_takes_all_of_it(m):
     k, n = 1040, 4096

@@ -39,3 +39,19 @@ def test_forward_with_the_least_workspace(m, columns):
     assert same(run(w, None, True, part), want)
     assert same(run(want[-2], want[-1], False, part), want[:-2])
     assert same(run(w, None, False, full), want[:-2])
+
+
+@pytest.mark.parametrize("m", [3, 40])
+def test_forward_without_columns(m):
+    """No output columns: nothing is done, and nothing needed, unless the column form of x is wanted."""
+    k = 272
+    x = torch.randn(m, k, device=DEV).to(torch.bfloat16)
+    F.linear_forward_fp8_block(x, None, 0, None, None, m, k, 0, F.FP8_E4M3, None, None, None, None, None, 0, None)
+    nbytes = F.linear_forward_fp8_block_workspace_size(m, k, 0)
+    ws = torch.full((nbytes + 256,), 0x7F, dtype=torch.uint8, device=DEV)
+    got, want = ([torch.zeros(m, k, dtype=torch.uint8, device=DEV), torch.zeros(1, k, device=DEV)] for _ in range(2))
+    F.linear_forward_fp8_block(x, None, 0, None, None, m, k, 0, F.FP8_E4M3, None, None, *got, ws, nbytes, None)
+    F.fp8_quantize_block(x, F.FP8_IN_BF16, m, k, F.FP8_E4M3, None, None, *want)
+    torch.cuda.synchronize()
+    assert F.fp8_get_device_status() == 0
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1]) and (ws[nbytes:] == 0x7F).all()
