@@ -2,6 +2,7 @@
 sizes, scales with strides of zero, outputs at any element, many batches, a very long contraction, the first call of a process
 made inside a capture, calls from several threads."""
 
+import os
 import subprocess
 import sys
 import threading
@@ -185,7 +186,9 @@ print("done")
                                          ("product", (1024, 1024, 256)), ("linear", (200, 272, 144)), ("experts", (2, 256, 144)),
                                          ("experts", (20, 256, 144))])
 def test_the_first_call_of_a_process_is_captured(which, sizes):
-    r = subprocess.run([sys.executable, "-c", FIRST.format(which=which, sizes=sizes)], capture_output=True, text=True, timeout=300)
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", FIRST.format(which=which, sizes=sizes)], capture_output=True, text=True, timeout=300,
+                       cwd=root)
     assert r.returncode == 0 and "done" in r.stdout, r.stderr[-2000:]
 
 
